@@ -359,6 +359,164 @@ int moe_zc_forward_host_fp8(const void* x_host, const void* W_r, const float* b,
                             const float* logit_offset, void* out_host, int64_t chunk_tokens,
                             void* stream);
 
+/*
+ * The layer learning.  The write-up trains the layer (sections
+ * "Zero-computation experts" and on the scaling strategy) but gives no
+ * formulas beyond the bias controller; the operators below are the plain
+ * derivatives of the layer defined above, a balance loss on the router's
+ * probabilities, and AdamW.  They use no workspace of the library's own and
+ * keep nothing between calls, so calls on different streams, and calls
+ * captured into different graphs, are independent; each is asynchronous on
+ * `stream` and allocates nothing.  All pointers are device memory unless said
+ * otherwise.  One training step of the router is
+ *   moe_zc_route_logits, moe_zc_dispatch, moe_zc_experts, moe_zc_combine
+ *   moe_zc_combine_backward   dout -> gradient of the gates (and of the rows)
+ *   moe_zc_balance_loss       the loss and its gradient's coefficients
+ *   moe_zc_route_backward     both -> gradient of the logits
+ *   (the caller's matrix products: dW_r = dlogits^T x, dx += dlogits W_r)
+ *   moe_zc_adamw              the step
+ * and dx's part through dispatch and combine is moe_zc_combine itself:
+ * zsum_t dout_t + sum_k dXrows[slot_{t,k}] (gates of 1).
+ */
+enum { MOE_ZC_F32 = 0, MOE_ZC_BF16 = 1 };   /* element types named below */
+
+/*
+ * moe_zc_route that also leaves the router's logits x W_r^T (before
+ * logit_offset) in logits [T, E] fp32, 16-byte aligned; everything else, bits
+ * included, as moe_zc_route.
+ */
+int moe_zc_route_logits(const void* x, const void* W_r, const float* b, const float* logit_offset,
+                        int64_t T, int32_t d, int32_t N, int32_t Z, int32_t K, float* logits,
+                        int32_t* idx, float* gate, float* zsum, int32_t* counts, void* stream);
+
+/*
+ * Balance loss of the router's softmax, per sequence, over all E experts
+ * (zero experts included).  With p_t = softmax(logits_t + logit_offset), n_s
+ * the counted tokens of sequence s and c_{s,i} the number of their picks on
+ * expert i:
+ *   P_{s,i} = (1 / n_s) sum_t p_{t,i}        f_{s,i} = w_i c_{s,i} / (K n_s)
+ *   loss_s  = sum_i f_{s,i} P_{s,i}          coef_{s,i} = f_{s,i} / n_s
+ * coef is d loss_s / d p_{t,i} (the counts are constants): what
+ * moe_zc_route_backward takes.
+ *   logits       [T, E] fp32 (e.g. moe_zc_route_logits), logit_offset [E] or NULL
+ *   idx          int32 [T, K] picks; entries outside [0, E) are not counted
+ *   mask         uint8 [T] or NULL: a token with 0 (padding) is not counted,
+ *                whatever its logits hold
+ *   seq_start    int32 [S + 1], nondecreasing: sequence s is the tokens
+ *                seq_start[s] .. seq_start[s + 1] - 1; tokens outside every
+ *                sequence are not counted; NULL: S must be 1, all T tokens
+ *   weight       fp32 [E] or NULL: w_i, the inverse of expert i's target
+ *                share of the picks; NULL: E for every expert.  The target of
+ *                the bias controller (zero experts rho of the picks together)
+ *                is w_i = N / (1 - rho) for i < N, Z / rho for i >= N.
+ *   loss, counts, prob, coef   fp32 [S], int32 [S, E], fp32 [S, E] (P), fp32
+ *                [S, E] out; all 0 for a sequence without counted tokens
+ *   workspace    workspace_bytes >= what moe_zc_balance_workspace gives,
+ *                16-byte aligned, the caller's until the stream's work is done
+ * Sums are fp32 in a fixed order: no float atomics, equal bits every run.
+ * T and S may be 0.  1 <= K <= min(E, 32), E <= 1024, T + S < 2^31; logits,
+ * logit_offset and coef 16-byte aligned.  For a loss over several ranks' tokens, sum counts
+ * and token numbers over the ranks and form coef from the sums.
+ */
+int moe_zc_balance_workspace(int64_t T, int32_t S, int32_t E, int64_t* bytes);
+int moe_zc_balance_loss(const float* logits, const float* logit_offset, const int32_t* idx,
+                        const uint8_t* mask, const int32_t* seq_start, const float* weight,
+                        int64_t T, int32_t S, int32_t E, int32_t K, float* loss, int32_t* counts,
+                        float* prob, float* coef, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+
+/*
+ * Gradient of the router's logits.  With p_t as above,
+ *   a_{t,i} = sum_{k: idx_{t,k} = i} dgate_{t,k} + dloss_s coef_{s,i}
+ *   dlogits_{t,i} = p_{t,i} (a_{t,i} - sum_j p_{t,j} a_{t,j})
+ * where s is the sequence of token t (no second term outside every sequence).
+ *   dgate     fp32 [T, K], the gradient of the gates (moe_zc_combine_backward),
+ *             or NULL (idx may then be NULL too); picks outside [0, E) add nothing
+ *   coef      fp32 [S, E] with dloss fp32 [S] (the loss's own gradient) and
+ *             seq_start as for moe_zc_balance_loss, or NULL
+ *   mask      uint8 [T] or NULL: a masked token's row of dlogits is 0,
+ *             whatever its logits and dgate hold
+ *   dlogits   [T, E] of the type `dtype` names (MOE_ZC_F32 or MOE_ZC_BF16,
+ *             rounded once); every row is written
+ * logits, logit_offset, coef and dlogits 16-byte aligned; sizes as for
+ * moe_zc_balance_loss.
+ */
+int moe_zc_route_backward(const float* logits, const float* logit_offset, const int32_t* idx,
+                          const float* dgate, const uint8_t* mask, const int32_t* seq_start,
+                          const float* coef, const float* dloss, int64_t T, int32_t S, int32_t E,
+                          int32_t K, void* dlogits, int32_t dtype, void* stream);
+
+/*
+ * Gradient of moe_zc_combine with respect to the gates and the rows:
+ *   dgate_{t,k} = dout_t . y_rows[slot_{t,k}]    slot >= 0
+ *               = dout_t . x_t                   slot < 0 (a zero expert's pick,
+ *                                                whose gate is part of zsum_t)
+ *   dy_rows[slot_{t,k}] = gate_{t,k} dout_t      slot >= 0
+ *   dout, x   bf16 [T, d]; y_rows bf16 [rows, d]; slot int32 [T, K] as
+ *             moe_zc_dispatch gives it (no row twice); gate fp32 [T, K]
+ *   dgate     fp32 [T, K] out (fp32 sums in a fixed order)
+ *   dy_rows   bf16 [rows, d] out, rounded once, or NULL (frozen experts; gate
+ *             may then be NULL); rows that no slot names are left as they were
+ * A slot >= rows is not followed and gives dgate 0.  d % 8 == 0, K <= 32, row
+ * buffers 16-byte aligned; y_rows may be NULL when rows is 0.
+ */
+int moe_zc_combine_backward(const void* dout, const void* x, const void* y_rows,
+                            const int32_t* slot, const float* gate, int64_t T, int32_t d,
+                            int32_t K, int64_t rows, float* dgate, void* dy_rows, void* stream);
+
+/*
+ * One AdamW step over n_tensors tensors at once.  Per element, with g =
+ * grad_scale * grad and n the number of this step:
+ *   m = beta1 m + (1 - beta1) g       v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr wd) - lr (m / (1 - beta1^n)) / (sqrt(v / (1 - beta2^n)) + eps)
+ * in fp32 (the bias corrections in fp64), lr = args->lr * lr_scale.
+ *   tensors   HOST array (read before the call returns) of device pointers;
+ *             n == 0 is allowed (its pointers may be NULL).  All have the types
+ *             args names.  param, grad, exp_avg, exp_avg_sq and master 16-byte
+ *             aligned; no two buffers that the step writes may overlap, nor may
+ *             a gradient overlap one.
+ *     master           fp32 weights (args->master = 1, param bf16): the step is
+ *                      taken there and param receives them rounded
+ *     state_bits 32    exp_avg = m and exp_avg_sq = v, fp32 [n]
+ *     state_bits 8     exp_avg holds m and exp_avg_sq holds sqrt(v), as E4M3
+ *                      codes uint8 [n] times one fp32 scale per
+ *                      MOE_ZC_ADAMW_BLOCK elements of the tensor
+ *                      (exp_avg_scale, exp_avg_sq_scale, fp32 [ceil(n / block)]):
+ *                      scale = max(amax, 2^-100) / 448, codes of value * (448 /
+ *                      max(amax, 2^-100)) to nearest, ties to even; a positive
+ *                      root never takes the code 0 (it would leave its m divided
+ *                      by eps alone).  A block holding an infinity or a NaN gets
+ *                      scale 1.  The step itself uses m and v before rounding.
+ *                      Zero codes are a fresh state.
+ *   step      int32 [2], device: [0] the steps done so far (n = step[0] + 1, and
+ *             the call advances it), [1] zero (the call's own counter, zero again
+ *             after it): a call captured into a graph goes on counting
+ *   lr_scale, grad_scale   fp32 device scalars or NULL (1)
+ * Requires 0 <= beta1, beta2 < 1, eps > 0.  One call at a time may use a given
+ * step counter.
+ */
+#define MOE_ZC_ADAMW_BLOCK 256
+typedef struct moe_zc_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  float* master;
+  int64_t n;
+} moe_zc_adamw_tensor;
+typedef struct moe_zc_adamw_args {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t param_type;   /* MOE_ZC_F32 or MOE_ZC_BF16 */
+  int32_t grad_type;
+  int32_t state_bits;   /* 32 or 8 */
+  int32_t master;       /* 1: master weights (param_type MOE_ZC_BF16) */
+} moe_zc_adamw_args;
+int moe_zc_adamw(const moe_zc_adamw_tensor* tensors, int32_t n_tensors,
+                 const moe_zc_adamw_args* args, int32_t* step, const float* lr_scale,
+                 const float* grad_scale, void* stream);
+
 /* Wait for the last forward; report (and clear) a device-side timeout. */
 int moe_zc_synchronize(void);
 

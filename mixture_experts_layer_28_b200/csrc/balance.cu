@@ -1,0 +1,322 @@
+// balance.cu -- the balance loss of the router's softmax and the gradient of
+// the logits.
+//
+// Per sequence s with n_s counted tokens (those of the sequence whose mask is
+// set), over all E experts, zero experts included:
+//   c_{s,i} = picks of expert i by those tokens          (not differentiated)
+//   P_{s,i} = (1/n_s) sum_t p_{t,i},   p_t = softmax(logits_t + offset)
+//   f_{s,i} = w_i c_{s,i} / (K n_s),   w_i = 1 / target share (E: an even load)
+//   loss_s  = sum_i f_{s,i} P_{s,i}
+//   coef_{s,i} = f_{s,i} / n_s = d loss_s / d p_{t,i}
+// and for the gradient, with dgate the gradient of the gates (p at the picks):
+//   a_{t,i}       = sum_{k: idx_{t,k} = i} dgate_{t,k} + dloss_s coef_{s,i}
+//   dlogits_{t,i} = p_{t,i} (a_{t,i} - sum_j p_{t,j} a_{t,j})
+//
+// Both directions read each logit once and are bound by that (and by the
+// gradient's store).  Nothing is reduced with float atomics: each block sums
+// the tokens of its own range in a fixed order and leaves partial sums, and a
+// second kernel adds those in block order, so results do not change from run
+// to run.
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace moezc {
+namespace {
+
+constexpr int BAL_WARPS = 8;
+constexpr int BAL_THREADS = BAL_WARPS * 32;
+
+// Offset s of the sequences, inside [0, T] whatever the caller's array holds.
+__device__ __forceinline__ int64_t seq_at(const int* __restrict__ seq, int s, int64_t T) {
+  if (!seq) return s == 0 ? 0 : T;
+  const int64_t v = seq[s];
+  return v < 0 ? 0 : (v > T ? T : v);
+}
+
+// Number of sequences whose end is at or before token t, i.e. the sequence
+// that holds t (or a later one, where t lies in a gap); one warp, 32 probes
+// per step.
+__device__ __forceinline__ int seq_of(const int* __restrict__ seq, int S, int64_t t, int64_t T,
+                                      int lane) {
+  int lo = 0, hi = S;            // answer in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int s = lo + lane * step;
+    const bool past = s < hi && seq_at(seq, s + 1, T) <= t;
+    const int k = __popc(__ballot_sync(0xffffffffu, past));   // probes at or before t
+    if (k == 0) return lo;
+    lo += (k - 1) * step + 1;
+    const int top = lo + step - 1;
+    hi = top < hi ? top : hi;
+  }
+  return lo;
+}
+
+// Partial sums of one (block, sequence) pair: block b's tokens of sequence s
+// go to slot b + s.  Walking the tokens, each step ends a block or a sequence,
+// so no two pairs share a slot and blocks + sequences slots are enough.
+template <int NV, bool VEC>
+__global__ void __launch_bounds__(BAL_THREADS)
+balance_partial_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
+                       const int* __restrict__ idx, const uint8_t* __restrict__ mask,
+                       const int* __restrict__ seq, int64_t T, int S, int E, int K, int chunk,
+                       float* __restrict__ psum, int* __restrict__ pcnt, int* __restrict__ pn) {
+  extern __shared__ float smem_f[];
+  float* red = smem_f;                                         // [BAL_WARPS][E]
+  int* hist = reinterpret_cast<int*>(smem_f + BAL_WARPS * E);  // [E]
+  __shared__ int nvalid[BAL_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
+  const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
+  int64_t t = t0;
+  for (int s = seq_of(seq, S, t0, T, lane); s < S && t < t1; ++s) {
+    const int64_t sa = seq_at(seq, s, T), se = seq_at(seq, s + 1, T);
+    const int64_t a = sa > t ? sa : t, e = se < t1 ? se : t1;
+    if (a >= t1) break;
+    if (a >= e) continue;
+    for (int j = threadIdx.x; j < E; j += BAL_THREADS) hist[j] = 0;
+    __syncthreads();
+    Row<NV> acc;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc.v[i][c] = 0.f;
+    int n = 0;
+    for (int64_t u = a + warp; u < e; u += BAL_WARPS) {
+      if (mask && !mask[u]) continue;
+      Row<NV> r;
+      row_load<NV, VEC>(r, logits + u * E, E, lane, -FLT_MAX);
+      const int pick = lane < K ? idx[u * K + lane] : -1;
+      row_softmax<NV, VEC>(r, offset, E, lane);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc.v[i][c] += r.v[i][c];
+      if (pick >= 0 && pick < E) atomicAdd(&hist[pick], 1);
+      ++n;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int j = 4 * lane + 128 * i + c;
+        if (j < E) red[warp * E + j] = acc.v[i][c];
+      }
+    if (lane == 0) nvalid[warp] = n;
+    __syncthreads();
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) + s) * E;
+    for (int j = threadIdx.x; j < E; j += BAL_THREADS) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < BAL_WARPS; ++w) sum += red[w * E + j];
+      psum[at + j] = sum;
+      pcnt[at + j] = hist[j];
+    }
+    if (threadIdx.x == 0) {
+      int m = 0;
+#pragma unroll
+      for (int w = 0; w < BAL_WARPS; ++w) m += nvalid[w];
+      pn[blockIdx.x + s] = m;
+    }
+    __syncthreads();
+    t = e;
+  }
+}
+
+// One block per sequence: partial sums added in block order.
+__global__ void __launch_bounds__(BAL_THREADS)
+balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcnt,
+                     const int* __restrict__ pn, const int* __restrict__ seq,
+                     const float* __restrict__ weight, int64_t T, int E, int K, int chunk,
+                     float* __restrict__ loss, int* __restrict__ counts, float* __restrict__ prob,
+                     float* __restrict__ coef) {
+  __shared__ float part[BAL_WARPS];
+  const int s = blockIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t a = seq_at(seq, s, T), e = seq_at(seq, s + 1, T);
+  const int64_t b0 = a / chunk, b1 = a < e ? (e - 1) / chunk + 1 : b0;
+  int64_t n = 0;
+  for (int64_t b = b0; b < b1; ++b) n += pn[b + s];
+  const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
+  float mine = 0.f;
+  for (int j = threadIdx.x; j < E; j += BAL_THREADS) {
+    float sum = 0.f;
+    int c = 0;
+    for (int64_t b = b0; b < b1; ++b) {
+      sum += psum[(b + s) * E + j];
+      c += pcnt[(b + s) * E + j];
+    }
+    const int64_t o = static_cast<int64_t>(s) * E + j;
+    const float P = sum * inv;
+    const float w = weight ? weight[j] : static_cast<float>(E);
+    const float f = static_cast<float>(c) * (w / static_cast<float>(K)) * inv;
+    counts[o] = c;
+    prob[o] = P;
+    coef[o] = f * inv;
+    mine += f * P;
+  }
+  mine = warp_sum(mine);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < BAL_WARPS; ++w) l += part[w];
+    loss[s] = l;
+  }
+}
+
+// Gradient of the logits: one warp per token.  The picks' dgate are added
+// into a row of shared memory per warp (zero between tokens).
+template <int NV, bool VEC, typename OUT>
+__global__ void __launch_bounds__(BAL_THREADS)
+route_backward_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
+                      const int* __restrict__ idx, const float* __restrict__ dgate,
+                      const uint8_t* __restrict__ mask, const int* __restrict__ seq,
+                      const float* __restrict__ coef, const float* __restrict__ dloss, int64_t T,
+                      int S, int E, int K, OUT* __restrict__ dlogits) {
+  extern __shared__ float smem_f[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* row = smem_f + warp * ((E + 3) & ~3);
+  for (int j = lane; j < E; j += 32) row[j] = 0.f;
+  __syncwarp();
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * BAL_WARPS + warp; t < T;
+       t += static_cast<int64_t>(gridDim.x) * BAL_WARPS) {
+    const bool on = !mask || mask[t];
+    int s = S;
+    if (on && coef) {
+      s = seq_of(seq, S, t, T, lane);
+      if (s < S && seq_at(seq, s, T) > t) s = S;   // a gap between sequences
+    }
+    Row<NV> a;
+    if (!on || (!dgate && s >= S)) {
+      // no gradient reaches this token (whatever its logits hold)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a.v[i][c] = 0.f;
+      row_store<NV, VEC>(a, dlogits + t * E, E, lane);
+      continue;
+    }
+    Row<NV> p;
+    row_load<NV, VEC>(p, logits + t * E, E, lane, -FLT_MAX);
+    int pick = -1;
+    if (dgate) {
+      float g = 0.f;
+      if (lane < K) {
+        pick = idx[t * K + lane];
+        g = dgate[t * K + lane];
+        if (pick < 0 || pick >= E) pick = -1;
+      }
+      // equal picks are added in k order by the first of them
+      const unsigned same = __match_any_sync(0xffffffffu, pick);
+      const int lead = __ffs(same) - 1;
+      float sum = g;
+      if (__any_sync(0xffffffffu, pick >= 0 && same != (1u << lane))) {
+        sum = 0.f;
+        for (int k = 0; k < K; ++k) {
+          const float gk = __shfl_sync(0xffffffffu, g, k);
+          if ((same >> k) & 1u) sum += gk;
+        }
+      }
+      if (pick >= 0 && lane == lead) row[pick] = sum;
+      __syncwarp();
+    }
+    row_softmax<NV, VEC>(p, offset, E, lane);
+    if (s < S) {
+      row_load<NV, VEC>(a, coef + static_cast<int64_t>(s) * E, E, lane, 0.f);
+      const float dl = dloss[s];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a.v[i][c] *= dl;
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a.v[i][c] = 0.f;
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int j = 4 * lane + 128 * i + c;
+        if (dgate && j < E) a.v[i][c] += row[j];
+        dot = fmaf(p.v[i][c], a.v[i][c], dot);
+      }
+    dot = warp_sum(dot);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) a.v[i][c] = p.v[i][c] * (a.v[i][c] - dot);
+    row_store<NV, VEC>(a, dlogits + t * E, E, lane);
+    __syncwarp();
+    if (pick >= 0) row[pick] = 0.f;
+    __syncwarp();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_balance_loss(const float* logits, const float* offset, const int* idx,
+                                const uint8_t* mask, const int* seq, const float* weight,
+                                int64_t T, int S, int E, int K, float* loss, int* counts,
+                                float* prob, float* coef, void* workspace, cudaStream_t stream) {
+  if (S <= 0) return cudaSuccess;
+  const BalancePlan pl = balance_plan(T, S, E);
+  char* ws = static_cast<char*>(workspace);
+  float* psum = reinterpret_cast<float*>(ws);
+  int* pcnt = reinterpret_cast<int*>(ws + pl.cnt_off);
+  int* pn = reinterpret_cast<int*>(ws + pl.n_off);
+  if (pl.blocks > 0) {
+    const size_t smem = static_cast<size_t>(BAL_WARPS + 1) * E * sizeof(float);
+    const cudaError_t e = with_row_shape(E, [&](auto nv, auto vec) {
+      constexpr auto kern = balance_partial_kernel<decltype(nv)::value, decltype(vec)::value != 0>;
+      return launch_pdl(kern, dim3(static_cast<unsigned>(pl.blocks)), dim3(BAL_THREADS), smem,
+                        stream, logits, offset, idx, mask, seq, T, S, E, K, pl.chunk, psum, pcnt,
+                        pn);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(balance_final_kernel, dim3(static_cast<unsigned>(S)), dim3(BAL_THREADS), 0,
+                    stream, psum, pcnt, pn, seq, weight, T, E, K, pl.chunk, loss, counts, prob,
+                    coef);
+}
+
+template <typename OUT>
+static cudaError_t route_backward_typed(const float* logits, const float* offset, const int* idx,
+                                        const float* dgate, const uint8_t* mask, const int* seq,
+                                        const float* coef, const float* dloss, int64_t T, int S,
+                                        int E, int K, OUT* dlogits, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(BAL_WARPS) * ((E + 3) & ~3) * sizeof(float);
+  return with_row_shape(E, [&](auto nv, auto vec) {
+    constexpr auto kern =
+        route_backward_kernel<decltype(nv)::value, decltype(vec)::value != 0, OUT>;
+    const int64_t want = (T + BAL_WARPS - 1) / BAL_WARPS;
+    const int64_t cap = static_cast<int64_t>(device_sms()) * blocks_per_sm<kern>(BAL_THREADS, smem);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(want < cap ? want : cap)),
+                      dim3(BAL_THREADS), smem, stream, logits, offset, idx, dgate, mask, seq, coef,
+                      dloss, T, S, E, K, dlogits);
+  });
+}
+
+cudaError_t launch_route_backward(const float* logits, const float* offset, const int* idx,
+                                  const float* dgate, const uint8_t* mask, const int* seq,
+                                  const float* coef, const float* dloss, int64_t T, int S, int E,
+                                  int K, void* dlogits, bool bf16, cudaStream_t stream) {
+  if (T <= 0) return cudaSuccess;
+  if (bf16)
+    return route_backward_typed(logits, offset, idx, dgate, mask, seq, coef, dloss, T, S, E, K,
+                                static_cast<__nv_bfloat16*>(dlogits), stream);
+  return route_backward_typed(logits, offset, idx, dgate, mask, seq, coef, dloss, T, S, E, K,
+                              static_cast<float*>(dlogits), stream);
+}
+
+}  // namespace moezc

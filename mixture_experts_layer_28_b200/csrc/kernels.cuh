@@ -334,9 +334,10 @@ cudaError_t launch_permute_fp8(const __nv_bfloat16* x, const int* idx, const int
 // softmax over E logits (+offset), + bias, top-K, zero-gate sums, histogram.
 // The logits may come as `splits` partial sums [splits][T][E], added in
 // slice order.
+// lout (optional, with splits > 1): the summed logits [T][E], before the offset.
 cudaError_t launch_route(const float* logits, const float* b, const float* offset, int64_t T,
                          int E, int N, int K, int* idx, float* gate, float* zsum, int* cnt,
-                         cudaStream_t stream, int splits = 1);
+                         cudaStream_t stream, int splits = 1, float* lout = nullptr);
 
 // ------------------------------------------------------------------ dispatch
 // Slot assignment with the experts' row and tile offsets (grp_off, grp_ttp
@@ -364,5 +365,62 @@ cudaError_t launch_permute(const __nv_bfloat16* x, const int* slot, int64_t T, i
 cudaError_t launch_combine(const __nv_bfloat16* x, const __nv_bfloat16* Y, const int* slot,
                            const float* gate, const float* zsum, int64_t T, int d, int K,
                            __nv_bfloat16* out, cudaStream_t stream);
+
+// ------------------------------------------------------------------ learning
+// The balance loss (balance.cu).  Tokens are cut into `blocks` ranges of
+// `chunk`; its workspace holds, for each of blocks + S (range, sequence)
+// slots, E partial sums, E partial counts and the number of counted tokens.
+// Two blocks per multiprocessor of a B200 when there are enough tokens, each
+// with at least one token per warp.
+struct BalancePlan {
+  int64_t blocks;
+  int chunk;
+  size_t cnt_off, n_off, bytes;
+};
+inline BalancePlan balance_plan(int64_t T, int S, int E) {
+  BalancePlan p;
+  const int64_t want = (T + 2 * 148 - 1) / (2 * 148);
+  p.chunk = static_cast<int>(want < 8 ? 8 : want);
+  p.blocks = (T + p.chunk - 1) / p.chunk;
+  const size_t slots = static_cast<size_t>(p.blocks) + S;
+  const size_t part = (slots * E * sizeof(float) + 255) / 256 * 256;
+  p.cnt_off = part;
+  p.n_off = 2 * part;
+  p.bytes = 2 * part + (slots * sizeof(int) + 255) / 256 * 256;
+  return p;
+}
+// seq: [S + 1] offsets or nullptr (S == 1: all T tokens).
+cudaError_t launch_balance_loss(const float* logits, const float* offset, const int* idx,
+                                const uint8_t* mask, const int* seq, const float* weight,
+                                int64_t T, int S, int E, int K, float* loss, int* counts,
+                                float* prob, float* coef, void* workspace, cudaStream_t stream);
+// dgate or coef (with dloss and seq) may be nullptr; dlogits fp32 or bf16.
+cudaError_t launch_route_backward(const float* logits, const float* offset, const int* idx,
+                                  const float* dgate, const uint8_t* mask, const int* seq,
+                                  const float* coef, const float* dloss, int64_t T, int S, int E,
+                                  int K, void* dlogits, bool bf16, cudaStream_t stream);
+// dY may be nullptr; rows: the rows of Y and dY (slots past them are not followed).
+cudaError_t launch_combine_backward(const __nv_bfloat16* dout, const __nv_bfloat16* x,
+                                    const __nv_bfloat16* Y, const int* slot, const float* gate,
+                                    int64_t T, int d, int K, int64_t rows, float* dgate,
+                                    __nv_bfloat16* dY, cudaStream_t stream);
+
+constexpr int ADAM_BLOCK = 256;   // elements per scale of an 8-bit state
+struct AdamTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;       // scales of 8-bit states, one per ADAM_BLOCK elements
+  float* vs;
+  float* master;   // fp32 weights (p bf16) or nullptr
+  int64_t n;
+};
+struct AdamHyper {
+  double lr, beta1, beta2, eps, weight_decay;
+};
+cudaError_t launch_adamw(const AdamTensor* t, int nt, bool p_bf16, bool g_bf16, bool master,
+                         bool bits8, const AdamHyper& h, int* step, const float* lr_scale,
+                         const float* grad_scale, cudaStream_t stream);
 
 }  // namespace moezc

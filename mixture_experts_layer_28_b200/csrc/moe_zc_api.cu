@@ -912,9 +912,11 @@ int moe_zc_forward_ex(const void* x, const void* W_r, const float* b, const void
                       stream);
 }
 
-int moe_zc_route(const void* x, const void* W_r, const float* b, const float* logit_offset,
-                 int64_t T, int32_t d, int32_t N, int32_t Z, int32_t K, int32_t* idx,
-                 float* gate, float* zsum, int32_t* counts, void* stream) {
+// moe_zc_route (logits_out NULL: the logits stay in the workspace) and
+// moe_zc_route_logits (logits_out: they are left there).
+static int route_impl(const void* x, const void* W_r, const float* b, const float* logit_offset,
+                      int64_t T, int32_t d, int32_t N, int32_t Z, int32_t K, float* logits_out,
+                      int32_t* idx, float* gate, float* zsum, int32_t* counts, void* stream) {
   const void* f = reinterpret_cast<const void*>(16);   // stand-ins: no expert weights here
   int s = check_args(x, W_r, b, f, f, f, T, d, N, Z, K, 128, logit_offset, f);
   if (s != MOE_ZC_OK) return s;
@@ -928,9 +930,13 @@ int moe_zc_route(const void* x, const void* W_r, const float* b, const float* lo
   const bool fresh_err = c.err.p == nullptr;
   if ((s = ensure(c, c.err, sizeof(int))) != MOE_ZC_OK) return s;
   if (fresh_err && cudaMemset(c.err.p, 0, sizeof(int)) != cudaSuccess) return MOE_ZC_ERR_CUDA;
-  if ((s = ensure(c, c.logits, static_cast<size_t>(T * E * rp.splits) * sizeof(float))) !=
-      MOE_ZC_OK)
+  // the router GEMM's output: the caller's array, unless there are K slices to sum
+  const bool direct = logits_out && rp.splits == 1;
+  if (!direct &&
+      (s = ensure(c, c.logits, static_cast<size_t>(T * E * rp.splits) * sizeof(float))) !=
+          MOE_ZC_OK)
     return s;
+  float* glogits = direct ? logits_out : static_cast<float*>(c.logits.p);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const long long wait_ns = g_wait_ns_next > 0 ? g_wait_ns_next : kWaitNs;
   g_wait_ns_next = 0;
@@ -947,7 +953,7 @@ int moe_zc_route(const void* x, const void* W_r, const float* b, const float* lo
     pr.T = static_cast<int>(T);
     pr.ksteps = d / GEMM_BK;
     pr.a_rows = E;
-    pr.out = c.logits.p;
+    pr.out = glogits;
     pr.out_ld = E;
     pr.err = static_cast<int*>(c.err.p);
     pr.wait_ns = wait_ns;
@@ -963,13 +969,32 @@ int moe_zc_route(const void* x, const void* W_r, const float* b, const float* lo
     const int64_t rg = rp.tiles * rp.splits;
     CK(launch_gemm(MODE_ROUTER, mWr, mWr, mX, mXf, pr, static_cast<int>(rg < c.sms ? rg : c.sms),
                    st));
-    CK(launch_route(static_cast<const float*>(c.logits.p), b, logit_offset, T, E, N, K, idx, gate,
-                    zsum, counts, st, rp.splits));
+    CK(launch_route(glogits, b, logit_offset, T, E, N, K, idx, gate, zsum, counts, st, rp.splits,
+                    direct ? nullptr : logits_out));
   }
-  CK(cudaEventRecord(c.done, st));
-  c.done_valid = true;
+  // (captured into a CUDA graph: no event, as in the forward)
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  CK(cudaStreamIsCapturing(st, &capturing));
+  c.done_valid = capturing == cudaStreamCaptureStatusNone;
+  if (c.done_valid) CK(cudaEventRecord(c.done, st));
   c.has_result = true;
   return MOE_ZC_OK;
+}
+
+int moe_zc_route(const void* x, const void* W_r, const float* b, const float* logit_offset,
+                 int64_t T, int32_t d, int32_t N, int32_t Z, int32_t K, int32_t* idx,
+                 float* gate, float* zsum, int32_t* counts, void* stream) {
+  return route_impl(x, W_r, b, logit_offset, T, d, N, Z, K, nullptr, idx, gate, zsum, counts,
+                    stream);
+}
+
+int moe_zc_route_logits(const void* x, const void* W_r, const float* b, const float* logit_offset,
+                        int64_t T, int32_t d, int32_t N, int32_t Z, int32_t K, float* logits,
+                        int32_t* idx, float* gate, float* zsum, int32_t* counts, void* stream) {
+  if (T > 0 && !logits) return MOE_ZC_ERR_INVALID_ARG;
+  if (!aligned16(logits)) return MOE_ZC_ERR_UNSUPPORTED;
+  return route_impl(x, W_r, b, logit_offset, T, d, N, Z, K, logits, idx, gate, zsum, counts,
+                    stream);
 }
 
 int moe_zc_dispatch(const void* x, const int32_t* idx, const int32_t* counts, int64_t T,

@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(ROUTE_WARPS * 32)
 route_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
              const float* __restrict__ offset, int64_t T, int E, int N, int K,
              int* __restrict__ idx, float* __restrict__ gate, float* __restrict__ zsum,
-             int* __restrict__ cnt, int splits, int tps) {
+             int* __restrict__ cnt, int splits, int tps, float* __restrict__ lout) {
   extern __shared__ int smem_i[];
   int* hist = smem_i;                                         // [E]
   float* lsum = reinterpret_cast<float*>(smem_i + E);         // [tps][E] (SLICED)
@@ -100,6 +100,13 @@ route_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
         l[i] = (j < E) ? lrow[j] : 0.f;
       }
     }
+    if (SLICED && lout && mine) {   // the summed logits are wanted too
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int j = lane + 32 * i;
+        if (j < E) lout[t * E + j] = l[i];
+      }
+    }
     if (mine) route_token<VPL>(l, bias, offset, E, N, K, lane, t, idx, gate, zsum, hist);
     if (SLICED && tps < ROUTE_WARPS) __syncthreads();   // lsum is refilled next step
   }
@@ -111,7 +118,8 @@ route_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
 template <int VPL, bool SLICED>
 cudaError_t launch_route_kernel(const float* logits, const float* b, const float* offset,
                                 int64_t T, int E, int N, int K, int* idx, float* gate,
-                                float* zsum, int* cnt, cudaStream_t stream, int splits) {
+                                float* zsum, int* cnt, cudaStream_t stream, int splits,
+                                float* lout) {
   const int sms = device_sms();
   // tokens per block step: ROUTE_WARPS, or for sliced logits of few tokens
   // fewer, so that about two blocks per SM share the slice sums
@@ -133,31 +141,31 @@ cudaError_t launch_route_kernel(const float* logits, const float* b, const float
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const int grid = static_cast<int>(want < cap ? want : cap);
   return launch_pdl(route_kernel<VPL, SLICED>, dim3(grid), dim3(ROUTE_WARPS * 32), smem, stream,
-                    logits, b, offset, T, E, N, K, idx, gate, zsum, cnt, splits, tps);
+                    logits, b, offset, T, E, N, K, idx, gate, zsum, cnt, splits, tps, lout);
 }
 
 template <int VPL>
 cudaError_t launch_route_vpl(const float* logits, const float* b, const float* offset, int64_t T,
                              int E, int N, int K, int* idx, float* gate, float* zsum, int* cnt,
-                             cudaStream_t stream, int splits) {
+                             cudaStream_t stream, int splits, float* lout) {
   if (splits > 1)
     return launch_route_kernel<VPL, true>(logits, b, offset, T, E, N, K, idx, gate, zsum, cnt,
-                                          stream, splits);
+                                          stream, splits, lout);
   return launch_route_kernel<VPL, false>(logits, b, offset, T, E, N, K, idx, gate, zsum, cnt,
-                                         stream, splits);
+                                         stream, splits, nullptr);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const float* logits, const float* b, const float* offset, int64_t T,
                          int E, int N, int K, int* idx, float* gate, float* zsum, int* cnt,
-                         cudaStream_t stream, int splits) {
+                         cudaStream_t stream, int splits, float* lout) {
   if (T <= 0) return cudaSuccess;
   if (splits < 1) splits = 1;
 #define MOEZC_ROUTE(V)                                                                     \
   if (E <= 32 * (V))                                                                       \
     return launch_route_vpl<V>(logits, b, offset, T, E, N, K, idx, gate, zsum, cnt, stream, \
-                               splits);
+                               splits, lout);
   MOEZC_ROUTE(1)
   MOEZC_ROUTE(2)
   MOEZC_ROUTE(3)
@@ -168,7 +176,8 @@ cudaError_t launch_route(const float* logits, const float* b, const float* offse
   MOEZC_ROUTE(16)
   MOEZC_ROUTE(24)
 #undef MOEZC_ROUTE
-  return launch_route_vpl<32>(logits, b, offset, T, E, N, K, idx, gate, zsum, cnt, stream, splits);
+  return launch_route_vpl<32>(logits, b, offset, T, E, N, K, idx, gate, zsum, cnt, stream, splits,
+                              lout);
 }
 
 }  // namespace moezc

@@ -7,9 +7,10 @@ the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence
 
 import numpy as np
 import torch
@@ -49,6 +50,23 @@ class LaunchPlan(ctypes.Structure):
                 ("expert_gemms_one_grid", ctypes.c_int32), ("expert_grid", ctypes.c_int32),
                 ("one_grid_step", ctypes.c_int32)]
 
+
+F32, BF16 = 0, 1            # MOE_ZC_F32, MOE_ZC_BF16
+ADAMW_BLOCK = 256           # elements per scale of an 8-bit AdamW state
+
+
+class AdamwArgs(ctypes.Structure):
+    """moe_zc_adamw_args (include/moe_zc.h)."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+                ("state_bits", ctypes.c_int32), ("master", ctypes.c_int32)]
+
+
+# moe_zc_adamw_tensor (include/moe_zc.h)
+_ADAMW_TENSOR = np.dtype([(k, np.int64) for k in ("param", "grad", "exp_avg", "exp_avg_sq",
+                                                  "exp_avg_scale", "exp_avg_sq_scale", "master",
+                                                  "n")])
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -122,6 +140,20 @@ def lib() -> ctypes.CDLL:
         L.moe_zc_experts.restype = ctypes.c_int
         L.moe_zc_combine.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, vp, vp]
         L.moe_zc_combine.restype = ctypes.c_int
+        L.moe_zc_route_logits.argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, vp, vp, vp,
+                                          vp, vp]
+        L.moe_zc_route_logits.restype = ctypes.c_int
+        L.moe_zc_balance_workspace.argtypes = [i64, i32, i32, vp]
+        L.moe_zc_balance_workspace.restype = ctypes.c_int
+        L.moe_zc_balance_loss.argtypes = [vp] * 6 + [i64, i32, i32, i32, vp, vp, vp, vp, vp, i64,
+                                                     vp]
+        L.moe_zc_balance_loss.restype = ctypes.c_int
+        L.moe_zc_route_backward.argtypes = [vp] * 8 + [i64, i32, i32, i32, vp, i32, vp]
+        L.moe_zc_route_backward.restype = ctypes.c_int
+        L.moe_zc_combine_backward.argtypes = [vp] * 5 + [i64, i32, i32, i64, vp, vp, vp]
+        L.moe_zc_combine_backward.restype = ctypes.c_int
+        L.moe_zc_adamw.argtypes = [vp, i32, ctypes.POINTER(AdamwArgs), vp, vp, vp, vp]
+        L.moe_zc_adamw.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -317,6 +349,271 @@ def combine(x: torch.Tensor, y_rows: torch.Tensor, slot: torch.Tensor, gate: tor
                                 _dev_ptr(out, torch.bfloat16, "out"), _stream_ptr(stream)),
            "moe_zc_combine")
     return out
+
+
+def _on(stream):
+    """Context in which what a call allocates belongs to the stream it runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
+    return torch.cuda.stream(stream)
+
+
+def _arg(t: Optional[torch.Tensor], dtype, shape, name: str) -> Optional[int]:
+    """Address of a contiguous tensor of this type and shape on the current device."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: torch.Tensor, N: int, Z: int, K: int,
+                 logit_offset: Optional[torch.Tensor] = None, stream=None):
+    """moe_zc_route_logits: (logits fp32 [T, E], idx, gate, zsum, counts), the
+    last four as route gives them."""
+    T, d = x.shape
+    E = N + Z
+    f32, bf, i32 = torch.float32, torch.bfloat16, torch.int32
+    args = (_arg(x, bf, (T, d), "x"), _arg(W_r, bf, (E, d), "W_r"), _arg(b, f32, (E,), "b"),
+            _arg(logit_offset, f32, (E,), "logit_offset"))
+    with _on(stream):
+        logits = torch.empty(T, E, dtype=f32, device=x.device)
+        idx = torch.empty(T, K, dtype=i32, device=x.device)
+        gate = torch.empty(T, K, dtype=f32, device=x.device)
+        zsum = torch.empty(T, dtype=f32, device=x.device)
+        counts = torch.empty(E, dtype=i32, device=x.device)
+    _check(lib().moe_zc_route_logits(*args, T, d, N, Z, K, logits.data_ptr(), idx.data_ptr(),
+                                     gate.data_ptr(), zsum.data_ptr(), counts.data_ptr(),
+                                     _stream_ptr(stream)), "moe_zc_route_logits")
+    return logits, idx, gate, zsum, counts
+
+
+class BalanceLoss(NamedTuple):
+    """What moe_zc_balance_loss computes."""
+    loss: torch.Tensor      # fp32 [S]
+    counts: torch.Tensor    # int32 [S, E]: counted tokens' picks per expert
+    prob: torch.Tensor      # fp32 [S, E]: mean router probability
+    coef: torch.Tensor      # fp32 [S, E]: d loss_s / d p_{t,i}, for route_backward
+
+
+def _row_args(logits, idx, logit_offset, mask, seq_start):
+    """Addresses and sizes that balance_loss and route_backward share."""
+    T, E = logits.shape
+    K = idx.shape[1] if idx is not None else 1
+    S = seq_start.numel() - 1 if seq_start is not None else 1
+    if S < 0:
+        raise ValueError("seq_start holds one offset more than there are sequences")
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"mask must be torch.bool or torch.uint8, got {mask.dtype}")
+    return T, E, K, S, (
+        _arg(logits, torch.float32, (T, E), "logits"),
+        _arg(logit_offset, torch.float32, (E,), "logit_offset"),
+        _arg(idx, torch.int32, (T, K), "idx"),
+        _arg(mask, mask.dtype, (T,), "mask") if mask is not None else None,
+        _arg(seq_start, torch.int32, (S + 1,), "seq_start"))
+
+
+def balance_loss(logits: torch.Tensor, idx: torch.Tensor,
+                 logit_offset: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                 seq_start: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                 stream=None) -> BalanceLoss:
+    """moe_zc_balance_loss: the balance loss of each sequence, with the
+    per-expert counts and the coefficients of its gradient.
+
+    logits fp32 [T, E] and idx int32 [T, K] as route_logits gives them; mask
+    (bool or uint8 [T]) drops padding tokens; seq_start (int32 [S + 1]) holds
+    the sequences' offsets (None: one sequence); weight (fp32 [E]) the inverse
+    target shares (None: an even load)."""
+    T, E, K, S, (lp, op, ip, mp, sp) = _row_args(logits, idx, logit_offset, mask, seq_start)
+    wp = _arg(weight, torch.float32, (E,), "weight")
+    nbytes = ctypes.c_int64(0)
+    _check(lib().moe_zc_balance_workspace(T, S, E, ctypes.byref(nbytes)),
+           "moe_zc_balance_workspace")
+    dev, f32 = logits.device, torch.float32
+    with _on(stream):
+        r = BalanceLoss(torch.empty(S, dtype=f32, device=dev),
+                        torch.empty(S, E, dtype=torch.int32, device=dev),
+                        torch.empty(S, E, dtype=f32, device=dev),
+                        torch.empty(S, E, dtype=f32, device=dev))
+        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
+    _check(lib().moe_zc_balance_loss(lp, op, ip, mp, sp, wp, T, S, E, K, r.loss.data_ptr(),
+                                     r.counts.data_ptr(), r.prob.data_ptr(), r.coef.data_ptr(),
+                                     ws.data_ptr(), nbytes.value, _stream_ptr(stream)),
+           "moe_zc_balance_loss")
+    return r
+
+
+def route_backward(logits: torch.Tensor, idx: Optional[torch.Tensor] = None,
+                   dgate: Optional[torch.Tensor] = None, coef: Optional[torch.Tensor] = None,
+                   dloss: Optional[torch.Tensor] = None,
+                   logit_offset: Optional[torch.Tensor] = None,
+                   mask: Optional[torch.Tensor] = None, seq_start: Optional[torch.Tensor] = None,
+                   dtype=torch.float32, stream=None) -> torch.Tensor:
+    """moe_zc_route_backward: gradient of the logits ([T, E], fp32 or bf16) from
+    the gates' gradient dgate (fp32 [T, K], with idx) and/or the balance loss's
+    (coef from balance_loss, dloss fp32 [S] the gradient of each loss_s).
+    Masked tokens get zeros."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+    if dgate is not None and idx is None:
+        raise ValueError("dgate needs idx")
+    if (coef is None) != (dloss is None):
+        raise ValueError("coef and dloss go together")
+    T, E, K, S, (lp, op, ip, mp, sp) = _row_args(logits, idx, logit_offset, mask, seq_start)
+    gp = _arg(dgate, torch.float32, (T, K), "dgate")
+    cp = _arg(coef, torch.float32, (S, E), "coef")
+    dp = _arg(dloss, torch.float32, (S,), "dloss")
+    with _on(stream):
+        out = torch.empty(T, E, dtype=dtype, device=logits.device)
+    if S == 0:
+        cp = dp = None   # no sequence, no loss
+    _check(lib().moe_zc_route_backward(lp, op, ip, gp, mp, sp, cp, dp, T, S, E, K, out.data_ptr(),
+                                       BF16 if dtype == torch.bfloat16 else F32,
+                                       _stream_ptr(stream)), "moe_zc_route_backward")
+    return out
+
+
+def combine_backward(dout: torch.Tensor, x: torch.Tensor, y_rows: torch.Tensor,
+                     slot: torch.Tensor, gate: torch.Tensor, rows: bool = True, stream=None):
+    """moe_zc_combine_backward: (dgate fp32 [T, K], dy_rows bf16 like y_rows, or
+    None with rows=False).  Rows of dy_rows that no slot names are not written."""
+    T, d = dout.shape
+    K = slot.shape[1]
+    R = y_rows.shape[0]
+    bf = torch.bfloat16
+    args = (_arg(dout, bf, (T, d), "dout"), _arg(x, bf, (T, d), "x"),
+            _arg(y_rows, bf, (R, d), "y_rows"), _arg(slot, torch.int32, (T, K), "slot"),
+            _arg(gate, torch.float32, (T, K), "gate"))
+    with _on(stream):
+        dgate = torch.empty(T, K, dtype=torch.float32, device=dout.device)
+        dy = torch.empty_like(y_rows) if rows else None
+    _check(lib().moe_zc_combine_backward(*args, T, d, K, R, dgate.data_ptr(),
+                                         dy.data_ptr() if rows else None, _stream_ptr(stream)),
+           "moe_zc_combine_backward")
+    return dgate, dy
+
+
+class Moment8(NamedTuple):
+    """An AdamW state of one tensor in 8 bits: E4M3 codes (uint8, the tensor's
+    shape) and an fp32 scale per ADAMW_BLOCK elements.  Zeros: a fresh state."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+class AdamW:
+    """AdamW over many tensors at once (moe_zc_adamw).
+
+    params: contiguous CUDA tensors of one type (bf16 or fp32) on one device,
+    16-byte aligned, updated in place.  state_bits 32 keeps fp32 moments, 8
+    keeps Moment8 of m and of sqrt(v).  exp_avg / exp_avg_sq: states to go on
+    from (fp32 tensors or Moment8, one per parameter; used in place), or None
+    for fresh ones.  master: fp32 weights, one per bf16 parameter, or True to
+    make them from params.  step: the steps done so far; the count lives on
+    the device (step_count), so a step captured into a CUDA graph goes on
+    counting in its replays.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float, betas=(0.9, 0.95),
+                 eps: float = 1e-8, weight_decay: float = 0.1, state_bits: int = 32,
+                 exp_avg=None, exp_avg_sq=None, master=None, step: int = 0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("params is empty")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        if not 0 <= step < 2 ** 31 - 1:
+            raise ValueError(f"step must be a count that fits int32, got {step}")
+        p0 = self.params[0]
+        if p0.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"params must be torch.float32 or torch.bfloat16, got {p0.dtype}")
+        self.device = p0.device
+        eight = state_bits == 8
+        if master is True:
+            master = [p.detach().to(torch.float32) for p in self.params]
+        if master is not None and p0.dtype != torch.bfloat16:
+            raise ValueError("master weights go with bf16 params")
+        self.exp_avg = self._states(exp_avg, eight)
+        self.exp_avg_sq = self._states(exp_avg_sq, eight)
+        self.master = list(master) if master is not None else None
+        for name in ("exp_avg", "exp_avg_sq", "master"):
+            v = getattr(self, name)
+            if v is not None and len(v) != len(self.params):
+                raise ValueError(f"{name} must hold one entry per parameter")
+        self._table = np.zeros(len(self.params), dtype=_ADAMW_TENSOR)
+        spans = []
+
+        def put(i, field, t, dtype, shape, name):
+            if t.device != self.device:
+                raise ValueError(f"{name}[{i}] must be on {self.device}")
+            self._table[field][i] = _arg(t, dtype, shape, f"{name}[{i}]")
+            if t.numel():
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
+
+        for i, p in enumerate(self.params):
+            n = p.numel()
+            self._table["n"][i] = n
+            put(i, "param", p, p0.dtype, p.shape, "params")
+            for field, v in (("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)):
+                if eight:
+                    put(i, field, v[i].codes, torch.uint8, p.shape, field)
+                    put(i, field + "_scale", v[i].scales, torch.float32,
+                        (-(-n // ADAMW_BLOCK),), field + " scales")
+                else:
+                    put(i, field, v[i], torch.float32, p.shape, field)
+            if self.master is not None:
+                put(i, "master", self.master[i], torch.float32, p.shape, "master")
+        spans.sort()
+        for (_, end), (start, _) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError("params and states must not overlap")
+        self.args = AdamwArgs(lr, betas[0], betas[1], eps, weight_decay,
+                              BF16 if p0.dtype == torch.bfloat16 else F32, F32, state_bits,
+                              1 if self.master is not None else 0)
+        self.step_count = torch.tensor([step, 0], dtype=torch.int32, device=self.device)
+
+    def _states(self, given, eight):
+        if given is not None:
+            return list(given)
+        if not eight:
+            return [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
+        return [Moment8(torch.zeros_like(p, dtype=torch.uint8),
+                        torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device))
+                for p in self.params]
+
+    def step(self, grads: Sequence[torch.Tensor], lr_scale: Optional[torch.Tensor] = None,
+             grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+        """One step on grads (one per parameter, its shape, all bf16 or all
+        fp32).  lr_scale and grad_scale are fp32 device tensors of one element
+        (a schedule's and a clipping factor), read when the step runs."""
+        if len(grads) != len(self.params):
+            raise ValueError("grads must hold one tensor per parameter")
+        gt = grads[0].dtype
+        if gt not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"grads must be torch.float32 or torch.bfloat16, got {gt}")
+        dev = self.device
+        if dev.index != torch.cuda.current_device():
+            raise ValueError(f"the current CUDA device must be {dev}")
+        ptrs = []
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if g.dtype != gt or g.shape != p.shape or g.device != dev or not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be a contiguous {gt} tensor of shape "
+                                 f"{tuple(p.shape)} on {dev}")
+            ptrs.append(g.data_ptr())
+        self._table["grad"] = ptrs
+        self.args.grad_type = BF16 if gt == torch.bfloat16 else F32
+        scales = [None if t is None else _arg(t.view(-1), torch.float32, (1,), name)
+                  for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale"))]
+        _check(lib().moe_zc_adamw(self._table.ctypes.data, len(ptrs), ctypes.byref(self.args),
+                                  self.step_count.data_ptr(), *scales, _stream_ptr(stream)),
+               "moe_zc_adamw")
 
 
 def forward_host(x_host: torch.Tensor, W_r: torch.Tensor, b: torch.Tensor,
