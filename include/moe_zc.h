@@ -414,7 +414,7 @@ int moe_zc_route_logits(const void* x, const void* W_r, const float* b, const fl
  *   workspace    workspace_bytes >= what moe_zc_balance_workspace gives,
  *                16-byte aligned, the caller's until the stream's work is done
  * Sums are fp32 in a fixed order: no float atomics, equal bits every run.
- * T and S may be 0.  1 <= K <= min(E, 32), E <= 1024, T + S < 2^31; logits,
+ * T and S may be 0.  1 <= K <= min(E, 32), E <= 1024, T + S < 2^31, S <= 2^27; logits,
  * logit_offset and coef 16-byte aligned.  For a loss over several ranks' tokens, sum counts
  * and token numbers over the ranks and form coef from the sums.
  */
@@ -492,7 +492,7 @@ int moe_zc_combine_backward(const void* dout, const void* x, const void* y_rows,
  *             the call advances it), [1] zero (the call's own counter, zero again
  *             after it): a call captured into a graph goes on counting
  *   lr_scale, grad_scale   fp32 device scalars or NULL (1)
- * Requires 0 <= beta1, beta2 < 1, eps > 0.  One call at a time may use a given
+ * Requires 0 <= beta1, beta2 < 1, eps >= 2^-126.  One call at a time may use a given
  * step counter.
  */
 #define MOE_ZC_ADAMW_BLOCK 256

@@ -126,46 +126,92 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
   }
 }
 
-// One block per sequence: partial sums added in block order.
-__global__ void __launch_bounds__(BAL_THREADS)
+// Partial sums added up: a cluster of CTAs per sequence (one wherever E <= 128),
+// each CTA 128 experts; thread (y, x) adds rows y, y + RG, ... of experts 4 x ..
+// 4 x + 3, then the RG sums are added in order, so that a few hundred rows are
+// a few loads deep instead of one long chain (one CTA per sequence walking all
+// rows took 121 us for 4 sequences of 4096 tokens, E = 768; this 4.6 us).  The
+// CTAs' parts of the loss meet in the first one's shared memory.
+template <int RG, bool VEC>
+__global__ void __launch_bounds__(RG * 32)
 balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcnt,
                      const int* __restrict__ pn, const int* __restrict__ seq,
-                     const float* __restrict__ weight, int64_t T, int E, int K, int chunk,
+                     const float* __restrict__ weight, int64_t T, int E, int K, int chunk, int nc,
                      float* __restrict__ loss, int* __restrict__ counts, float* __restrict__ prob,
                      float* __restrict__ coef) {
-  __shared__ float part[BAL_WARPS];
-  const int s = blockIdx.x;
+  __shared__ float4 sum_s[RG][32];
+  __shared__ int4 cnt_s[RG][32];
+  __shared__ float part[4];          // warps 0..3: their experts' part of the loss
+  __shared__ float cta_part[8];      // (first CTA) the CTAs' parts
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int s = blockIdx.x / nc, rank = blockIdx.x % nc;
   griddep_wait();
   griddep_launch_dependents();
   const int64_t a = seq_at(seq, s, T), e = seq_at(seq, s + 1, T);
   const int64_t b0 = a / chunk, b1 = a < e ? (e - 1) / chunk + 1 : b0;
-  int64_t n = 0;
-  for (int64_t b = b0; b < b1; ++b) n += pn[b + s];
-  const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
-  float mine = 0.f;
-  for (int j = threadIdx.x; j < E; j += BAL_THREADS) {
-    float sum = 0.f;
-    int c = 0;
-    for (int64_t b = b0; b < b1; ++b) {
-      sum += psum[(b + s) * E + j];
-      c += pcnt[(b + s) * E + j];
-    }
-    const int64_t o = static_cast<int64_t>(s) * E + j;
-    const float P = sum * inv;
-    const float w = weight ? weight[j] : static_cast<float>(E);
-    const float f = static_cast<float>(c) * (w / static_cast<float>(K)) * inv;
-    counts[o] = c;
-    prob[o] = P;
-    coef[o] = f * inv;
-    mine += f * P;
-  }
-  mine = warp_sum(mine);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = mine;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float l = 0.f;
+  const int64_t r0 = b0 + s, rows = b1 - b0;     // this sequence's slots
+  const int j0 = rank * 128 + 4 * x;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  int c[4] = {0, 0, 0, 0};
+  if (j0 < E) {
+#pragma unroll 4
+    for (int64_t r = y; r < rows; r += RG) {
+      const float* ps = psum + (r0 + r) * E + j0;
+      const int* pc = pcnt + (r0 + r) * E + j0;
+      if (VEC) {
+        const float4 f = *reinterpret_cast<const float4*>(ps);
+        const int4 q = *reinterpret_cast<const int4*>(pc);
+        v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+        c[0] += q.x; c[1] += q.y; c[2] += q.z; c[3] += q.w;
+      } else {
 #pragma unroll
-    for (int w = 0; w < BAL_WARPS; ++w) l += part[w];
+        for (int i = 0; i < 4; ++i)
+          if (j0 + i < E) {
+            v[i] += ps[i];
+            c[i] += pc[i];
+          }
+      }
+    }
+  }
+  sum_s[y][x] = make_float4(v[0], v[1], v[2], v[3]);
+  cnt_s[y][x] = make_int4(c[0], c[1], c[2], c[3]);
+  int nt = 0;                                    // counted tokens
+  if (y < 4)
+    for (int64_t r = x; r < rows; r += 32) nt += pn[r0 + r];
+  __syncthreads();
+  if (y < 4) {
+    const int n = __reduce_add_sync(0xffffffffu, nt);
+    const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
+    const int j = rank * 128 + threadIdx.x;
+    float mine = 0.f;
+    if (j < E) {
+      float sum = 0.f;
+      int cn = 0;
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+        sum += reinterpret_cast<const float*>(sum_s[g])[threadIdx.x];
+        cn += reinterpret_cast<const int*>(cnt_s[g])[threadIdx.x];
+      }
+      const int64_t o = static_cast<int64_t>(s) * E + j;
+      const float P = sum * inv;
+      const float w = weight ? weight[j] : static_cast<float>(E);
+      const float f = static_cast<float>(cn) * (w / static_cast<float>(K)) * inv;
+      counts[o] = cn;
+      prob[o] = P;
+      coef[o] = f * inv;
+      mine = f * P;
+    }
+    mine = warp_sum(mine);
+    if (x == 0) part[y] = mine;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    st_cluster_u32(mapa_shared(smem_u32(&cta_part[rank]), 0),
+                   __float_as_uint(part[0] + part[1] + part[2] + part[3]));
+  cluster_sync_all();
+  if (rank == 0 && threadIdx.x == 0) {
+    float l = 0.f;
+    for (int r = 0; r < nc; ++r) l += cta_part[r];
     loss[s] = l;
   }
 }
@@ -285,9 +331,19 @@ cudaError_t launch_balance_loss(const float* logits, const float* offset, const 
     });
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(balance_final_kernel, dim3(static_cast<unsigned>(S)), dim3(BAL_THREADS), 0,
-                    stream, psum, pcnt, pn, seq, weight, T, E, K, pl.chunk, loss, counts, prob,
-                    coef);
+  // row groups: 32 where a sequence has many rows to add, 8 for short ones
+  int nc = 1;
+  while (nc * 128 < E) nc *= 2;
+  const bool many = (pl.blocks + S) / S > 16;
+  auto final_stage = [&](auto rg, auto vec) {
+    constexpr auto kern = balance_final_kernel<decltype(rg)::value, decltype(vec)::value != 0>;
+    return launch_pdl_cluster(kern, nc, dim3(static_cast<unsigned>(S) * nc),
+                              dim3(decltype(rg)::value * 32), 0, stream, psum, pcnt, pn, seq,
+                              weight, T, E, K, pl.chunk, nc, loss, counts, prob, coef);
+  };
+  if (E % 4 == 0)
+    return many ? final_stage(IntC<32>{}, IntC<1>{}) : final_stage(IntC<8>{}, IntC<1>{});
+  return many ? final_stage(IntC<32>{}, IntC<0>{}) : final_stage(IntC<8>{}, IntC<0>{});
 }
 
 template <typename OUT>

@@ -28,6 +28,7 @@ int check_rows(int64_t T, int32_t S, int32_t E, int32_t K) {
   if (T < 0 || S < 0 || E < 1 || K < 1 || K > E) return MOE_ZC_ERR_INVALID_ARG;
   if (K > MOE_ZC_MAX_K || E > MOE_ZC_MAX_E) return MOE_ZC_ERR_UNSUPPORTED;
   if (T > 0x7fffffffLL - S) return MOE_ZC_ERR_UNSUPPORTED;   // (offsets are int32)
+  if (S > (1 << 27)) return MOE_ZC_ERR_UNSUPPORTED;           // (8 CTAs each)
   return MOE_ZC_OK;
 }
 
@@ -113,7 +114,7 @@ int moe_zc_adamw(const moe_zc_adamw_tensor* tensors, int32_t n_tensors,
     return MOE_ZC_ERR_INVALID_ARG;
   // (written so that a NaN fails)
   if (!(a.beta1 >= 0.0 && a.beta1 < 1.0) || !(a.beta2 >= 0.0 && a.beta2 < 1.0) ||
-      !(static_cast<float>(a.eps) > 0.f) || !std::isfinite(a.eps) || !std::isfinite(a.lr) ||
+      !(static_cast<float>(a.eps) >= 0x1p-126f) || !std::isfinite(a.eps) || !std::isfinite(a.lr) ||
       !std::isfinite(a.weight_decay))
     return MOE_ZC_ERR_INVALID_ARG;
   if (!aligned(step, 4) || !aligned(lr_scale, 4) || !aligned(grad_scale, 4))
