@@ -485,8 +485,8 @@ int moe_zc_combine_backward(const void* dout, const void* x, const void* y_rows,
  *                      scale = max(amax, 2^-100) / 448, codes of value * (448 /
  *                      max(amax, 2^-100)) to nearest, ties to even; a positive
  *                      root never takes the code 0 (it would leave its m divided
- *                      by eps alone).  A block holding an infinity or a NaN gets
- *                      scale 1.  The step itself uses m and v before rounding.
+ *                      by eps alone).  A block holding a NaN, an infinity or
+ *                      2^126 and more gets scale 1.  The step itself uses m and v before rounding.
  *                      Zero codes are a fresh state.
  *   step      int32 [2], device: [0] the steps done so far (n = step[0] + 1, and
  *             the call advances it), [1] zero (the call's own counter, zero again

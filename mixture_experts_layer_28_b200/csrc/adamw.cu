@@ -15,11 +15,19 @@
 // two, so that a block whose gradients stop decays by b every step although
 // its codes stand still.
 //
-// Bound by the bytes of weights, gradients and states.  The tensors' addresses
-// travel in the launch's parameters (no copy to the device, so a captured step
-// replays as it is), a block takes units of ADAM_UNIT elements of the
-// concatenated tensors, and the step count lives on the device: the last block
-// to have read it moves it on.
+// Bound by the bytes of weights, gradients and states; the 8-bit step (10 bytes
+// per element) has only some 50 issue slots per element for them, so its
+// arithmetic runs in packed fp32 pairs and without branches.  A block takes
+// units of the concatenated tensors in turn; each warp loads GROUPS groups of
+// 256 elements at once, whole vectors side by side, before it computes any of
+// them.  Small blocks (128 threads) that wait for nobody keep the memory
+// busiest: staging units through shared memory, by cp.async or by bulk copies
+// both ways, was slower for 8-bit states (403M elements: 0.92 and 0.83 ms against
+// 0.72).
+//
+// The tensors' addresses travel in the launch's parameters (no copy to the
+// device, so a captured step replays as it is), and the step count lives on the
+// device: the last block to have read it moves it on.
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -30,11 +38,6 @@
 namespace moezc {
 namespace {
 
-constexpr int ADAM_THREADS = 256;
-constexpr int ADAM_WARPS = ADAM_THREADS / 32;
-constexpr int ADAM_GROUPS = 2;   // 256-element groups (8 a lane) a warp has in flight
-constexpr int ADAM_WARP_ELEMS = ADAM_GROUPS * ADAM_BLOCK;
-constexpr int ADAM_UNIT = ADAM_WARPS * ADAM_WARP_ELEMS;   // elements a block takes at a time
 static_assert(ADAM_BLOCK == 256, "one scale per 8 elements of each lane of a warp");
 
 template <int MAXT>
@@ -95,6 +98,17 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// 1 / sqrt(x) to about an ulp, for normal x.
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 // Maximum that keeps a NaN (as the largest bits).
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -102,135 +116,155 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Eight consecutive elements as they sit in memory, loaded (the first n of
-// them, the rest zero; FULL: all eight) before anything is computed from them.
-template <typename E>
-struct Raw8;
-template <>
-struct Raw8<float> {
-  float4 a, b;
+// A lane's eight elements of a group of ADAM_BLOCK.  SPLIT (where fp32 arrays
+// are read): elements 4 l .. 4 l + 3 and 128 + 4 l .., so that a warp's 16-byte
+// accesses lie side by side; else 8 l .. 8 l + 7.
+template <bool SPLIT>
+__device__ __forceinline__ int elem(int lane, int i) {
+  return SPLIT ? 4 * lane + (i & 3) + (i >> 2) * 128 : 8 * lane + i;
+}
+
+__device__ __forceinline__ uint32_t bits_of(const float* p) { return __float_as_uint(*p); }
+__device__ __forceinline__ uint32_t bits_of(const __nv_bfloat16* p) {
+  return *reinterpret_cast<const uint16_t*>(p);
+}
+__device__ __forceinline__ uint32_t bits_of(const uint8_t* p) { return *p; }
+
+// Those elements as they sit in memory: all loaded before any is computed with.
+// (fp32 and split accesses are marked as streamed: 26 against 29 us at 4.7M
+// weights with fp32 states; the whole vectors of the 8-bit step are not: 0.70
+// against 0.71 ms at 403M.)
+// FULL: the whole group lies in the tensor; else only its first n elements, one
+// by one (the rest are zero).
+template <typename E, bool SPLIT>
+struct Raw8 {
+  static constexpr int W = 2 * sizeof(E);   // 32-bit words
+  uint32_t w[W];
   template <bool FULL>
-  __device__ __forceinline__ void load(const float* p, int n) {
-    if (FULL) {
-      a = __ldcs(reinterpret_cast<const float4*>(p));
-      b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  __device__ __forceinline__ void load(const E* p, int lane, int n) {
+    if (!FULL) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = elem<SPLIT>(lane, i);
+        constexpr int PER = 4 / sizeof(E);   // elements of a word
+        if (e < n) w[i / PER] |= bits_of(p + e) << (8 * sizeof(E) * (i % PER));
+      }
+    } else if constexpr (sizeof(E) == 4) {
+      put4(0, __ldcs(reinterpret_cast<const uint4*>(p + elem<SPLIT>(lane, 0))));
+      put4(4, __ldcs(reinterpret_cast<const uint4*>(p + elem<SPLIT>(lane, 4))));
+    } else if constexpr (sizeof(E) == 2 && !SPLIT) {
+      put4(0, *reinterpret_cast<const uint4*>(p + elem<SPLIT>(lane, 0)));
+    } else if constexpr (sizeof(E) == 2) {
+      put2(0, __ldcs(reinterpret_cast<const uint2*>(p + elem<SPLIT>(lane, 0))));
+      put2(2, __ldcs(reinterpret_cast<const uint2*>(p + elem<SPLIT>(lane, 4))));
+    } else if constexpr (!SPLIT) {
+      put2(0, *reinterpret_cast<const uint2*>(p + elem<SPLIT>(lane, 0)));
     } else {
-      a = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f,
-                      n > 3 ? p[3] : 0.f);
-      b = make_float4(n > 4 ? p[4] : 0.f, n > 5 ? p[5] : 0.f, n > 6 ? p[6] : 0.f,
-                      n > 7 ? p[7] : 0.f);
+      w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p + elem<SPLIT>(lane, 0)));
+      w[1] = __ldcs(reinterpret_cast<const uint32_t*>(p + elem<SPLIT>(lane, 4)));
     }
   }
-  __device__ __forceinline__ void get(F2 (&v)[4]) const {
-    v[0] = pk(a.x, a.y); v[1] = pk(a.z, a.w);
-    v[2] = pk(b.x, b.y); v[3] = pk(b.z, b.w);
-  }
-};
-template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 q;
-  template <bool FULL>
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int n) {
-    if (FULL) {
-      q = __ldcs(reinterpret_cast<const uint4*>(p));
-    } else {
-      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) w[i >> 1] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
-      q = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  __device__ __forceinline__ void get(F2 (&v)[4]) const {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = pk(bf16_lo(w[i]), bf16_hi(w[i]));
-  }
-};
-// Eight E4M3 codes (get: in units of their scale).
-template <>
-struct Raw8<uint8_t> {
-  uint2 q;
-  template <bool FULL>
-  __device__ __forceinline__ void load(const uint8_t* p, int n) {
-    if (FULL) {
-      q = __ldcs(reinterpret_cast<const uint2*>(p));
-    } else {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-      q = make_uint2(w[0], w[1]);
-    }
-  }
+  // E4M3 codes: in units of their scale
   __device__ __forceinline__ void get(F2 (&v)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w = i < 2 ? q.x : q.y;
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-          static_cast<__nv_fp8x2_storage_t>(w >> (16 * (i & 1))), __NV_E4M3);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      v[i] = pk(f.x, f.y);
+      if constexpr (sizeof(E) == 4) {
+        v[i] = pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      } else if constexpr (sizeof(E) == 2) {
+        v[i] = pk(bf16_lo(w[i]), bf16_hi(w[i]));
+      } else {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        v[i] = pk(f.x, f.y);
+      }
     }
+  }
+  __device__ __forceinline__ void set(const F2 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = up(v[i]);
+      if constexpr (sizeof(E) == 4) {
+        w[2 * i] = __float_as_uint(f.x);
+        w[2 * i + 1] = __float_as_uint(f.y);
+      } else if constexpr (sizeof(E) == 2) {
+        const __nv_bfloat162 h = __float22bfloat162_rn(f);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const uint32_t q = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+        w[i >> 1] = (i & 1) ? w[i >> 1] | (q << 16) : q;
+      }
+    }
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void store(E* p, int lane, int n) const {
+    if (!FULL) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = elem<SPLIT>(lane, i);
+        constexpr int PER = 4 / sizeof(E);
+        const uint32_t b = w[i / PER] >> (8 * sizeof(E) * (i % PER));
+        if (e < n) {
+          if constexpr (sizeof(E) == 4) *reinterpret_cast<uint32_t*>(p + e) = b;
+          else if constexpr (sizeof(E) == 2) *reinterpret_cast<uint16_t*>(p + e) = static_cast<uint16_t>(b);
+          else *reinterpret_cast<uint8_t*>(p + e) = static_cast<uint8_t>(b);
+        }
+      }
+    } else if constexpr (sizeof(E) == 4) {
+      __stcs(reinterpret_cast<uint4*>(p + elem<SPLIT>(lane, 0)), make_uint4(w[0], w[1], w[2], w[3]));
+      __stcs(reinterpret_cast<uint4*>(p + elem<SPLIT>(lane, 4)), make_uint4(w[4], w[5], w[6], w[7]));
+    } else if constexpr (sizeof(E) == 2 && !SPLIT) {
+      *reinterpret_cast<uint4*>(p + elem<SPLIT>(lane, 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (sizeof(E) == 2) {
+      __stcs(reinterpret_cast<uint2*>(p + elem<SPLIT>(lane, 0)), make_uint2(w[0], w[1]));
+      __stcs(reinterpret_cast<uint2*>(p + elem<SPLIT>(lane, 4)), make_uint2(w[2], w[3]));
+    } else if constexpr (!SPLIT) {
+      *reinterpret_cast<uint2*>(p + elem<SPLIT>(lane, 0)) = make_uint2(w[0], w[1]);
+    } else {
+      __stcs(reinterpret_cast<uint32_t*>(p + elem<SPLIT>(lane, 0)), w[0]);
+      __stcs(reinterpret_cast<uint32_t*>(p + elem<SPLIT>(lane, 4)), w[1]);
+    }
+  }
+
+ private:
+  __device__ __forceinline__ void put4(int i, uint4 q) {
+    w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+  }
+  __device__ __forceinline__ void put2(int i, uint2 q) {
+    w[i] = q.x; w[i + 1] = q.y;
   }
 };
 
-template <bool FULL>
-__device__ __forceinline__ void put8(const F2 (&v)[4], float* p, int n) {
-  const float2 a = up(v[0]), b = up(v[1]), c = up(v[2]), d = up(v[3]);
-  if (FULL) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(a.x, a.y, b.x, b.y));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(c.x, c.y, d.x, d.y));
-  } else {
-    const float f[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = f[i];
-  }
-}
-template <bool FULL>
-__device__ __forceinline__ void put8(const F2 (&v)[4], __nv_bfloat16* p, int n) {
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(up(v[i]));
-  if (FULL) {
-    __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(h));
-  } else {
-    const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(h);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = e[i];
-  }
-}
-// Codes of values in units of their scale (|v| <= 448 up to rounding).
-template <bool FULL>
-__device__ __forceinline__ void put8(const F2 (&v)[4], uint8_t* p, int n) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(up(v[2 * i]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(up(v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    w[i] = lo | (hi << 16);
-  }
-  if (FULL) {
-    __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
-  }
+// Square roots of two values >= 0 by Heron's method: from s = v y, y within
+// about an ulp of 1 / sqrt(v), one step s + (v - s^2) / (2 s), whose residual
+// an fma gives exactly; what is left is the last rounding's.  No branch, so the
+// eight roots of a lane run side by side (the library's root, which tests its
+// argument, cost 0.1 ms of 0.9 at 403M elements).  0 stays 0, a NaN a NaN; an
+// overflow counts as the largest float, and below 2^-126 (gradients under
+// 1e-19) the root comes out too small, by 2 at 2^-130.
+__device__ __forceinline__ F2 sqrt2(F2 v) {
+  const float2 a = up(v);
+  const float lo = 0x1p-126f, hi = 3.402823466e+38f;
+  const F2 y = pk(rsqrt_approx(fmaxf(a.x, lo)), rsqrt_approx(fmaxf(a.y, lo)));
+  const F2 x = pk(min_nan(a.x, hi), min_nan(a.y, hi));
+  const F2 s = mul2(x, y);
+  const F2 e = fma2(mul2(s, pk(-1.f, -1.f)), s, x);
+  return fma2(e, mul2(y, pk(0.5f, 0.5f)), s);
 }
 
 // Scale of a block from its largest magnitude (bits of a non-negative float,
-// or of an infinity or NaN), and the factor to units of it.  A block holding
-// an infinity or a NaN gets scale 1 (a NaN keeps the NaN code, an infinity
+// or of an infinity or NaN), and the factor to units of it, 448 / amax through
+// one Newton step of the reciprocal.  A block holding an infinity, a NaN or
+// 2^126 and more gets scale 1 (a NaN keeps the NaN code, what is too large
 // saturates); the floor keeps 448 / amax finite.
 __device__ __forceinline__ float block_scale(uint32_t amax_bits, float& inv) {
-  const bool finite = amax_bits < 0x7F800000u;
-  const float a = finite ? fmaxf(__uint_as_float(amax_bits), 0x1p-100f) : 448.0f;
-  inv = finite ? __fmul_rn(__frcp_rn(a), 448.0f) : 1.0f;
-  return finite ? __fmul_rn(a, 1.0f / 448.0f) : 1.0f;
+  const bool fine = amax_bits < 0x7E800000u;
+  const float a = fmaxf(__uint_as_float(fine ? amax_bits : 0u), 0x1p-100f);
+  const float y = rcp_approx(a);
+  inv = fine ? __fmul_rn(fmaf(fmaf(-a, y, 1.0f), y, y), 448.0f) : 1.0f;
+  return fine ? __fmul_rn(a, 1.0f / 448.0f) : 1.0f;
 }
 
 struct Coef {
@@ -248,58 +282,76 @@ __device__ __forceinline__ void adam8(F2 (&p)[4], const F2 (&g)[4], F2 (&m)[4], 
     const F2 gi = mul2(g[i], c.gscale);
     m[i] = add2(mul2(m[i], c.b1), mul2(gi, c.omb1));
     v[i] = add2(mul2(v[i], c.b2), mul2(mul2(gi, gi), c.omb2));
-    const float2 vi = up(v[i]);
-    r[i] = pk(__fsqrt_rn(vi.x), __fsqrt_rn(vi.y));
+    r[i] = sqrt2(v[i]);
     const float2 den = up(fma2(r[i], c.rs, c.eps));
     const F2 q = mul2(m[i], pk(rcp_approx(den.x), rcp_approx(den.y)));
     p[i] = fma2(q, c.neg_step, mul2(p[i], c.decay));
   }
 }
 
-// One warp's ADAM_GROUPS groups of a tensor from element e0 (a multiple of
-// ADAM_BLOCK) on.  FULL: all of them lie inside the tensor.
-template <typename PT, typename GT, bool MASTER, bool BITS8, bool FULL>
-__device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int lane,
-                                          const Coef& c) {
+// The types of a launch and what follows from them.
+template <typename PT_, typename GT_, bool MASTER_, bool BITS8_>
+struct Types {
+  using PT = PT_;
+  using GT = GT_;
+  static constexpr bool MASTER = MASTER_, BITS8 = BITS8_;
   using WT = typename std::conditional<MASTER, float, PT>::type;   // the weight stepped on
   using ST = typename std::conditional<BITS8, uint8_t, float>::type;
-  WT* w = (MASTER ? reinterpret_cast<WT*>(T.master) : static_cast<WT*>(T.p)) + e0 + 8 * lane;
-  PT* pp = static_cast<PT*>(T.p) + e0 + 8 * lane;
-  const GT* gp = static_cast<const GT*>(T.g) + e0 + 8 * lane;
-  ST* mp = static_cast<ST*>(T.m) + e0 + 8 * lane;
-  ST* vp = static_cast<ST*>(T.v) + e0 + 8 * lane;
+  static constexpr bool SPLIT = sizeof(WT) == 4 || sizeof(GT) == 4 || !BITS8;
+  static constexpr int THREADS = 128;
+  static constexpr int WARPS = THREADS / 32;
+  // a warp's groups in flight (8 bits: 12 bytes a lane and element fewer, so two;
+  // measured 0.701 against 0.784 ms with one at 403M elements, bf16; fp32 states:
+  // 206 against 220 us with one at 60M)
+  static constexpr int GROUPS = BITS8 ? 2 : 1;
+  static constexpr int BLOCKS = 7;    // resident blocks per SM (72 registers)
+  static constexpr int UE = WARPS * GROUPS * ADAM_BLOCK;   // elements of a unit
+};
+
+// A warp's GROUPS groups of a tensor from element e0 (a multiple of ADAM_BLOCK)
+// on.  FULL: all of them lie inside the tensor.
+template <typename Y, bool FULL>
+__device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int lane,
+                                          const Coef& c) {
+  using WT = typename Y::WT;
+  using ST = typename Y::ST;
+  constexpr int NG = Y::GROUPS;
+  constexpr bool SP = Y::SPLIT;
+  WT* w = (Y::MASTER ? reinterpret_cast<WT*>(T.master) : static_cast<WT*>(T.p)) + e0;
+  typename Y::PT* pp = static_cast<typename Y::PT*>(T.p) + e0;
+  const typename Y::GT* gp = static_cast<const typename Y::GT*>(T.g) + e0;
+  ST* mp = static_cast<ST*>(T.m) + e0;
+  ST* vp = static_cast<ST*>(T.v) + e0;
   const int64_t b0 = e0 / ADAM_BLOCK;
-  Raw8<WT> rp[ADAM_GROUPS];
-  Raw8<GT> rg[ADAM_GROUPS];
-  Raw8<ST> rm[ADAM_GROUPS], rv[ADAM_GROUPS];
-  float sm[ADAM_GROUPS], sv[ADAM_GROUPS];
-  int n[ADAM_GROUPS];        // this lane's elements of the group
-  bool there[ADAM_GROUPS];   // the group has any (uniform)
+  Raw8<WT, SP> rp[NG];
+  Raw8<typename Y::GT, SP> rg[NG];
+  Raw8<ST, SP> rm[NG], rv[NG];
+  float sm[NG], sv[NG];
+  int n[NG];        // elements of the group (FULL: not used)
 #pragma unroll
-  for (int k = 0; k < ADAM_GROUPS; ++k) {
+  for (int k = 0; k < NG; ++k) {
     const int o = k * ADAM_BLOCK;
-    const int64_t left = FULL ? 8 : T.n - (e0 + o + 8 * lane);
-    n[k] = left >= 8 ? 8 : (left > 0 ? static_cast<int>(left) : 0);
-    there[k] = FULL || e0 + o < T.n;
-    rp[k].template load<FULL>(w + o, n[k]);
-    rg[k].template load<FULL>(gp + o, n[k]);
-    rm[k].template load<FULL>(mp + o, n[k]);
-    rv[k].template load<FULL>(vp + o, n[k]);
-    if (BITS8) {
-      sm[k] = there[k] ? T.ms[b0 + k] : 0.f;
-      sv[k] = there[k] ? T.vs[b0 + k] : 0.f;
+    const int64_t left = FULL ? ADAM_BLOCK : T.n - (e0 + o);
+    n[k] = left >= ADAM_BLOCK ? ADAM_BLOCK : (left > 0 ? static_cast<int>(left) : 0);
+    rp[k].template load<FULL>(w + o, lane, n[k]);
+    rg[k].template load<FULL>(gp + o, lane, n[k]);
+    rm[k].template load<FULL>(mp + o, lane, n[k]);
+    rv[k].template load<FULL>(vp + o, lane, n[k]);
+    if (Y::BITS8) {
+      sm[k] = n[k] > 0 ? T.ms[b0 + k] : 0.f;
+      sv[k] = n[k] > 0 ? T.vs[b0 + k] : 0.f;
     }
   }
 #pragma unroll
-  for (int k = 0; k < ADAM_GROUPS; ++k) {
+  for (int k = 0; k < NG; ++k) {
     const int o = k * ADAM_BLOCK;
-    if (!there[k]) break;
+    if (!FULL && n[k] == 0) break;
     F2 p[4], g[4], m[4], v[4], r[4];
     rp[k].get(p);
     rg[k].get(g);
     rm[k].get(m);
     rv[k].get(v);
-    if (BITS8) {
+    if (Y::BITS8) {
       const F2 s2 = pk(sm[k], sm[k]), t2 = pk(sv[k], sv[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -309,12 +361,14 @@ __device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int l
       }
     }
     adam8(p, g, m, v, r, c);
-    if (MASTER) put8<FULL>(p, w + o, n[k]);
-    put8<FULL>(p, pp + o, n[k]);
-    if constexpr (!BITS8) {
-      put8<FULL>(m, mp + o, n[k]);
-      put8<FULL>(v, vp + o, n[k]);
-    } else {
+    rp[k].set(p);
+    rp[k].template store<FULL>(w + o, lane, n[k]);
+    if (Y::MASTER) {
+      Raw8<typename Y::PT, SP> out;
+      out.set(p);
+      out.template store<FULL>(pp + o, lane, n[k]);
+    }
+    if (Y::BITS8) {
       // (elements past the tensor's end are zero: their m and r stay zero)
       float fm = 0.f, fr = 0.f, low = 0x1p+120f;
 #pragma unroll
@@ -331,25 +385,27 @@ __device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int l
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         m[i] = mul2(m[i], im2);
-        r[i] = mul2(r[i], ir2);
+        v[i] = mul2(r[i], ir2);
       }
       // a positive root never gets the code of zero (few blocks span that much)
       if (low * ir < 0x1p-9f) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 b = up(r[i]);
+          float2 b = up(v[i]);
           b.x = b.x > 0.f ? fmaxf(b.x, 0x1p-9f) : b.x;
           b.y = b.y > 0.f ? fmaxf(b.y, 0x1p-9f) : b.y;
-          r[i] = pk(b.x, b.y);
+          v[i] = pk(b.x, b.y);
         }
       }
-      put8<FULL>(m, mp + o, n[k]);
-      put8<FULL>(r, vp + o, n[k]);
       if (lane == 0) {
         T.ms[b0 + k] = nm;
         T.vs[b0 + k] = nr;
       }
     }
+    rm[k].set(m);
+    rv[k].set(v);
+    rm[k].template store<FULL>(mp + o, lane, n[k]);
+    rv[k].template store<FULL>(vp + o, lane, n[k]);
   }
 }
 
@@ -358,8 +414,8 @@ __device__ __forceinline__ F2 both(double x) {
   return pk(f, f);
 }
 
-template <typename PT, typename GT, bool MASTER, bool BITS8, int MAXT>
-__global__ void __launch_bounds__(ADAM_THREADS)
+template <typename Y, int MAXT>
+__global__ void __launch_bounds__(Y::THREADS, Y::BLOCKS)
 adamw_kernel(const __grid_constant__ AdamArgs<MAXT> a) {
   __shared__ Coef coef_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -389,32 +445,38 @@ adamw_kernel(const __grid_constant__ AdamArgs<MAXT> a) {
   __syncthreads();
   const Coef c = coef_s;
   const int units = a.unit_end[a.nt - 1];
+  int ti = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    int ti = 0;   // the first tensor whose units end after u
-    for (int hi = a.nt - 1; ti < hi;) {
-      const int mid = (ti + hi) >> 1;
-      if (a.unit_end[mid] > u) hi = mid; else ti = mid + 1;
+    if (u >= a.unit_end[ti]) {   // the first tensor whose units end after u
+      int hi = a.nt - 1;
+      for (++ti; ti < hi;) {
+        const int mid = (ti + hi) >> 1;
+        if (a.unit_end[mid] > u) hi = mid; else ti = mid + 1;
+      }
     }
     const AdamTensor& T = a.t[ti];
     const int u0 = ti ? a.unit_end[ti - 1] : 0;
-    const int64_t e0 = static_cast<int64_t>(u - u0) * ADAM_UNIT + warp * ADAM_WARP_ELEMS;
-    if (e0 + ADAM_WARP_ELEMS <= T.n)
-      adam_warp<PT, GT, MASTER, BITS8, true>(T, e0, lane, c);
+    const int64_t e0 =
+        static_cast<int64_t>(u - u0) * Y::UE + warp * (Y::GROUPS * ADAM_BLOCK);
+    if (e0 + Y::GROUPS * ADAM_BLOCK <= T.n)
+      adam_warp<Y, true>(T, e0, lane, c);
     else if (e0 < T.n)
-      adam_warp<PT, GT, MASTER, BITS8, false>(T, e0, lane, c);
+      adam_warp<Y, false>(T, e0, lane, c);
   }
   griddep_launch_dependents();
 }
 
-template <typename PT, typename GT, bool MASTER, bool BITS8, int MAXT>
+template <typename Y, int MAXT>
 cudaError_t launch_some(const AdamTensor* t, int nt, bool advance, const AdamHyper& h, int* step,
                         const float* lr_scale, const float* grad_scale, cudaStream_t stream) {
+  constexpr auto kern = adamw_kernel<Y, MAXT>;
+  const int64_t cap = static_cast<int64_t>(device_sms()) * blocks_per_sm<kern>(Y::THREADS, 0);
   AdamArgs<MAXT> a;
   int64_t units = 0;
   for (int i = 0; i < nt; ++i) {
     a.t[i] = t[i];
-    units += (t[i].n + ADAM_UNIT - 1) / ADAM_UNIT;
-    if (units > 0x7fffffff) return cudaErrorInvalidValue;
+    units += (t[i].n + Y::UE - 1) / Y::UE;
+    if (units > 0x7fffffff - cap) return cudaErrorInvalidValue;
     a.unit_end[i] = static_cast<int>(units);
   }
   a.nt = nt;
@@ -423,26 +485,23 @@ cudaError_t launch_some(const AdamTensor* t, int nt, bool advance, const AdamHyp
   a.step = step;
   a.lr_scale = lr_scale;
   a.grad_scale = grad_scale;
-  constexpr auto kern = adamw_kernel<PT, GT, MASTER, BITS8, MAXT>;
-  const int64_t cap = static_cast<int64_t>(device_sms()) * blocks_per_sm<kern>(ADAM_THREADS, 0);
   const int64_t grid = units < cap ? (units > 0 ? units : 1) : cap;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(ADAM_THREADS), 0, stream, a);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(Y::THREADS), 0, stream, a);
 }
 
 // Tensors of one launch: as many as its parameters (32764 bytes at most) hold.
 constexpr int ADAM_FEW = 16, ADAM_MANY = 448;
 static_assert(sizeof(AdamArgs<ADAM_MANY>) <= 32764, "kernel parameters");
 
-template <typename PT, typename GT, bool MASTER, bool BITS8>
+template <typename Y>
 cudaError_t launch_all(const AdamTensor* t, int nt, const AdamHyper& h, int* step,
                        const float* lr_scale, const float* grad_scale, cudaStream_t stream) {
   if (nt <= ADAM_FEW)
-    return launch_some<PT, GT, MASTER, BITS8, ADAM_FEW>(t, nt, true, h, step, lr_scale, grad_scale,
-                                                        stream);
+    return launch_some<Y, ADAM_FEW>(t, nt, true, h, step, lr_scale, grad_scale, stream);
   for (int i = 0; i < nt; i += ADAM_MANY) {
     const int k = nt - i < ADAM_MANY ? nt - i : ADAM_MANY;
-    const cudaError_t e = launch_some<PT, GT, MASTER, BITS8, ADAM_MANY>(
-        t + i, k, i + k == nt, h, step, lr_scale, grad_scale, stream);
+    const cudaError_t e = launch_some<Y, ADAM_MANY>(t + i, k, i + k == nt, h, step, lr_scale,
+                                                    grad_scale, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -452,13 +511,16 @@ template <typename PT, bool MASTER>
 cudaError_t launch_typed(const AdamTensor* t, int nt, bool g_bf16, bool bits8, const AdamHyper& h,
                          int* step, const float* lr_scale, const float* grad_scale,
                          cudaStream_t stream) {
+  using B = __nv_bfloat16;
   if (g_bf16)
-    return bits8 ? launch_all<PT, __nv_bfloat16, MASTER, true>(t, nt, h, step, lr_scale,
-                                                               grad_scale, stream)
-                 : launch_all<PT, __nv_bfloat16, MASTER, false>(t, nt, h, step, lr_scale,
-                                                                grad_scale, stream);
-  return bits8 ? launch_all<PT, float, MASTER, true>(t, nt, h, step, lr_scale, grad_scale, stream)
-               : launch_all<PT, float, MASTER, false>(t, nt, h, step, lr_scale, grad_scale, stream);
+    return bits8 ? launch_all<Types<PT, B, MASTER, true>>(t, nt, h, step, lr_scale, grad_scale,
+                                                          stream)
+                 : launch_all<Types<PT, B, MASTER, false>>(t, nt, h, step, lr_scale, grad_scale,
+                                                           stream);
+  return bits8 ? launch_all<Types<PT, float, MASTER, true>>(t, nt, h, step, lr_scale, grad_scale,
+                                                            stream)
+               : launch_all<Types<PT, float, MASTER, false>>(t, nt, h, step, lr_scale, grad_scale,
+                                                             stream);
 }
 
 }  // namespace

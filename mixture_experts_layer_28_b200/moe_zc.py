@@ -611,9 +611,9 @@ class AdamW:
         self.args.grad_type = BF16 if gt == torch.bfloat16 else F32
         scales = [None if t is None else _arg(t.view(-1), torch.float32, (1,), name)
                   for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale"))]
+        st = _stream_ptr(stream)
         _check(lib().moe_zc_adamw(self._table.ctypes.data, len(ptrs), ctypes.byref(self.args),
-                                  self.step_count.data_ptr(), *scales, _stream_ptr(stream)),
-               "moe_zc_adamw")
+                                  self.step_count.data_ptr(), *scales, st), "moe_zc_adamw")
 
 
 def forward_host(x_host: torch.Tensor, W_r: torch.Tensor, b: torch.Tensor,

@@ -451,6 +451,22 @@ def test_adamw_tiny_and_huge_values(bits):
     assert torch.allclose(w, torch.full_like(w, -1e-2), rtol=1e-5)
 
 
+def test_adamw_roots_at_the_edges():
+    """sqrt(v) as the 8-bit state sees it (beta2 = 0, one element per block, so a
+    block's scale is its root / 448): within 2 u of the exact root from the
+    smallest normal float to the largest, and exactly the zero block's at v = 0."""
+    e = torch.linspace(-62.5, 63.9, 1500, dtype=torch.float64)
+    g = torch.zeros(1501, 256)
+    g[1:, 0] = (2.0 ** e).float()
+    w = torch.zeros(1501 * 256, device="cuda")
+    opt = mz.AdamW([w], lr=1e-3, betas=(0.0, 0.0), eps=1e-30, weight_decay=0.0, state_bits=8)
+    opt.step([g.view(-1).cuda()])
+    scale = opt.exp_avg_sq[0].scales.cpu().double()
+    v = (g[:, 0] * g[:, 0]).double()     # (rounded as the kernel rounds it)
+    assert scale[0] == 2.0 ** -100 / 448 or abs(scale[0] * 448 / 2.0 ** -100 - 1) < 2 * U
+    assert ((scale[1:] * 448 / v[1:].sqrt().clamp(min=2.0 ** -100) - 1).abs() <= 4 * U).all()
+
+
 def test_adamw_step_count_and_scales():
     """Ten steps with a device-side schedule equal the float64 recurrence."""
     params, grads = adam_case([1000], torch.float32, torch.float32)
