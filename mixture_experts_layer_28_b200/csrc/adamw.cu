@@ -29,6 +29,7 @@
 // device, so a captured step replays as it is), and the step count lives on the
 // device: the last block to have read it moves it on.
 #include "kernels.cuh"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 #include <cuda_fp8.h>
@@ -62,42 +63,6 @@ __device__ __forceinline__ double one_minus_pow(double b, int n) {
   return 1.0 - r;
 }
 
-// Pairs of fp32 values in one 64-bit register: the packed instructions round
-// each half like their scalar forms and take one issue slot for both, which is
-// what the 8-bit step is short of (DRAM feeds 2.3 elements per clock and SM,
-// 55 scalar issue slots each).
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pk(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 up(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-// 1 / x to about an ulp, for normal x.
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // 1 / sqrt(x) to about an ulp, for normal x.
 __device__ __forceinline__ float rsqrt_approx(float x) {
   float r;
@@ -409,11 +374,6 @@ __device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int l
   }
 }
 
-__device__ __forceinline__ F2 both(double x) {
-  const float f = static_cast<float>(x);
-  return pk(f, f);
-}
-
 template <typename Y, int MAXT>
 __global__ void __launch_bounds__(Y::THREADS, Y::BLOCKS)
 adamw_kernel(const __grid_constant__ AdamArgs<MAXT> a) {
@@ -424,14 +384,14 @@ adamw_kernel(const __grid_constant__ AdamArgs<MAXT> a) {
     const int n = *reinterpret_cast<volatile int*>(a.step) + 1;
     const double lr = a.h.lr * (a.lr_scale ? *a.lr_scale : 1.0f);
     Coef c;
-    c.b1 = both(a.h.beta1);
-    c.omb1 = both(1.0 - a.h.beta1);
-    c.b2 = both(a.h.beta2);
-    c.omb2 = both(1.0 - a.h.beta2);
-    c.eps = both(a.h.eps);
-    c.decay = both(1.0 - lr * a.h.weight_decay);
-    c.neg_step = both(-lr / one_minus_pow(a.h.beta1, n));
-    c.rs = both(rsqrt(one_minus_pow(a.h.beta2, n)));
+    c.b1 = both(static_cast<float>(a.h.beta1));
+    c.omb1 = both(static_cast<float>(1.0 - a.h.beta1));
+    c.b2 = both(static_cast<float>(a.h.beta2));
+    c.omb2 = both(static_cast<float>(1.0 - a.h.beta2));
+    c.eps = both(static_cast<float>(a.h.eps));
+    c.decay = both(static_cast<float>(1.0 - lr * a.h.weight_decay));
+    c.neg_step = both(static_cast<float>(-lr / one_minus_pow(a.h.beta1, n)));
+    c.rs = both(static_cast<float>(rsqrt(one_minus_pow(a.h.beta2, n))));
     c.gscale = both(a.grad_scale ? *a.grad_scale : 1.0f);
     coef_s = c;
     if (a.advance) {

@@ -34,6 +34,24 @@ __device__ __forceinline__ int64_t seq_at(const int* __restrict__ seq, int s, in
   return v < 0 ? 0 : (v > T ? T : v);
 }
 
+// A row into shared memory (E % 4 == 0: 16-byte aligned rows).
+template <int NV, bool VEC>
+__device__ __forceinline__ void row_put(const Row<NV>& r, float* dst, int E, int lane) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = 4 * lane + 128 * i;
+    const float2 a = up(r.v[i][0]), b = up(r.v[i][1]);
+    if (VEC) {
+      if (j < E) *reinterpret_cast<float4*>(dst + j) = make_float4(a.x, a.y, b.x, b.y);
+    } else {
+      if (j < E) dst[j] = a.x;
+      if (j + 1 < E) dst[j + 1] = a.y;
+      if (j + 2 < E) dst[j + 2] = b.x;
+      if (j + 3 < E) dst[j + 3] = b.y;
+    }
+  }
+}
+
 // Number of sequences whose end is at or before token t, i.e. the sequence
 // that holds t (or a later one, where t lies in a gap); one warp, 32 probes
 // per step.
@@ -62,7 +80,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
                        const int* __restrict__ idx, const uint8_t* __restrict__ mask,
                        const int* __restrict__ seq, int64_t T, int S, int E, int K, int chunk,
                        float* __restrict__ psum, int* __restrict__ pcnt, int* __restrict__ pn) {
-  extern __shared__ float smem_f[];
+  extern __shared__ __align__(16) float smem_f[];
   float* red = smem_f;                                         // [BAL_WARPS][E]
   int* hist = reinterpret_cast<int*>(smem_f + BAL_WARPS * E);  // [E]
   __shared__ int nvalid[BAL_WARPS];
@@ -80,31 +98,35 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
     for (int j = threadIdx.x; j < E; j += BAL_THREADS) hist[j] = 0;
     __syncthreads();
     Row<NV> acc;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc.v[i][c] = 0.f;
+    acc.fill(0.f);
     int n = 0;
+    // the next token's row is on its way while this one is summed
+    Row<NV> nxt;
+    int nxt_pick = -1;
+    bool nxt_on = true;
+    auto fetch = [&](int64_t u) {
+      if (u >= e) return;
+      row_load<NV, VEC>(nxt, logits + u * E, E, lane, -INFINITY);
+      nxt_pick = lane < K ? idx[u * K + lane] : -1;
+      nxt_on = !mask || mask[u];
+    };
+    fetch(a + warp);
     for (int64_t u = a + warp; u < e; u += BAL_WARPS) {
-      if (mask && !mask[u]) continue;
-      Row<NV> r;
-      row_load<NV, VEC>(r, logits + u * E, E, lane, -FLT_MAX);
-      const int pick = lane < K ? idx[u * K + lane] : -1;
-      row_softmax<NV, VEC>(r, offset, E, lane);
+      Row<NV> r = nxt;
+      const int pick = nxt_pick;
+      const bool on = nxt_on;
+      fetch(u + BAL_WARPS);
+      if (!on) continue;
+      row_exp<NV, VEC>(r, offset, E, lane);
+      const F2 inv = both(1.0f / warp_sum(row_lane_sum(r)));
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc.v[i][c] += r.v[i][c];
+        for (int h = 0; h < 2; ++h) acc.v[i][h] = fma2(r.v[i][h], inv, acc.v[i][h]);
       if (pick >= 0 && pick < E) atomicAdd(&hist[pick], 1);
       ++n;
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int j = 4 * lane + 128 * i + c;
-        if (j < E) red[warp * E + j] = acc.v[i][c];
-      }
+    row_put<NV, VEC>(acc, red + warp * E, E, lane);
     if (lane == 0) nvalid[warp] = n;
     __syncthreads();
     const int64_t at = (static_cast<int64_t>(blockIdx.x) + s) * E;
@@ -216,50 +238,69 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
   }
 }
 
-// Gradient of the logits: one warp per token.  The picks' dgate are added
-// into a row of shared memory per warp (zero between tokens).
+// Gradient of the logits: one warp per token, a block a range of `chunk`
+// consecutive tokens, so that a warp finds its sequence once and then again
+// only at a boundary.  The picks' dgate are added into a row of shared memory
+// per warp (zero between tokens).
 template <int NV, bool VEC, typename OUT>
 __global__ void __launch_bounds__(BAL_THREADS)
 route_backward_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                       const int* __restrict__ idx, const float* __restrict__ dgate,
                       const uint8_t* __restrict__ mask, const int* __restrict__ seq,
                       const float* __restrict__ coef, const float* __restrict__ dloss, int64_t T,
-                      int S, int E, int K, OUT* __restrict__ dlogits) {
-  extern __shared__ float smem_f[];
+                      int S, int E, int K, int chunk, OUT* __restrict__ dlogits) {
+  extern __shared__ __align__(16) float smem_f[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* row = smem_f + warp * ((E + 3) & ~3);
   for (int j = lane; j < E; j += 32) row[j] = 0.f;
   __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * BAL_WARPS + warp; t < T;
-       t += static_cast<int64_t>(gridDim.x) * BAL_WARPS) {
-    const bool on = !mask || mask[t];
-    int s = S;
-    if (on && coef) {
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
+  const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
+  // the next token's row is on its way while this one is worked on
+  Row<NV> nxt;
+  int nxt_pick = -1;
+  float nxt_g = 0.f;
+  bool nxt_on = true;
+  auto fetch = [&](int64_t t) {
+    if (t >= t1) return;
+    row_load<NV, VEC>(nxt, logits + t * E, E, lane, -INFINITY);
+    nxt_on = !mask || mask[t];
+    if (dgate && lane < K) {
+      nxt_pick = idx[t * K + lane];
+      nxt_g = dgate[t * K + lane];
+    }
+  };
+  fetch(t0 + warp);
+  // tokens [sa, se) share s (S: no sequence); none known yet
+  int s = S;
+  int64_t sa = 0, se = coef ? 0 : T;
+  for (int64_t t = t0 + warp; t < t1; t += BAL_WARPS) {
+    Row<NV> p = nxt;
+    int pick = nxt_pick;
+    const float g = nxt_g;
+    const bool on = nxt_on;
+    fetch(t + BAL_WARPS);
+    if (t < sa || t >= se) {
       s = seq_of(seq, S, t, T, lane);
-      if (s < S && seq_at(seq, s, T) > t) s = S;   // a gap between sequences
+      sa = s < S ? seq_at(seq, s, T) : t;
+      se = s < S ? seq_at(seq, s + 1, T) : T;
+      if (sa > t) {   // a gap before sequence s
+        se = sa;
+        sa = t;
+        s = S;
+      }
     }
     Row<NV> a;
     if (!on || (!dgate && s >= S)) {
       // no gradient reaches this token (whatever its logits hold)
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) a.v[i][c] = 0.f;
+      a.fill(0.f);
       row_store<NV, VEC>(a, dlogits + t * E, E, lane);
       continue;
     }
-    Row<NV> p;
-    row_load<NV, VEC>(p, logits + t * E, E, lane, -FLT_MAX);
-    int pick = -1;
     if (dgate) {
-      float g = 0.f;
-      if (lane < K) {
-        pick = idx[t * K + lane];
-        g = dgate[t * K + lane];
-        if (pick < 0 || pick >= E) pick = -1;
-      }
+      if (pick < 0 || pick >= E) pick = -1;
       // equal picks are added in k order by the first of them
       const unsigned same = __match_any_sync(0xffffffffu, pick);
       const int lead = __ffs(same) - 1;
@@ -273,39 +314,40 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
       }
       if (pick >= 0 && lane == lead) row[pick] = sum;
       __syncwarp();
-    }
-    row_softmax<NV, VEC>(p, offset, E, lane);
-    if (s < S) {
-      row_load<NV, VEC>(a, coef + static_cast<int64_t>(s) * E, E, lane, 0.f);
-      const float dl = dloss[s];
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) a.v[i][c] *= dl;
+      row_load<NV, VEC>(a, row, E, lane, 0.f);
+      __syncwarp();
+      if (pick >= 0) row[pick] = 0.f;
+      __syncwarp();
     } else {
+      a.fill(0.f);
+    }
+    if (s < S) {
+      Row<NV> c;
+      row_load<NV, VEC>(c, coef + static_cast<int64_t>(s) * E, E, lane, 0.f);
+      const F2 dl = both(dloss[s]);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) a.v[i][c] = 0.f;
+        for (int h = 0; h < 2; ++h) a.v[i][h] = fma2(c.v[i][h], dl, a.v[i][h]);
     }
-    float dot = 0.f;
+    // with e = exp(l - max): p = e / sum e, sum_j p_j a_j = (sum_j e_j a_j) / sum e
+    row_exp<NV, VEC>(p, offset, E, lane);
+    F2 ea = mul2(p.v[0][0], a.v[0][0]);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int j = 4 * lane + 128 * i + c;
-        if (dgate && j < E) a.v[i][c] += row[j];
-        dot = fmaf(p.v[i][c], a.v[i][c], dot);
-      }
-    dot = warp_sum(dot);
+      for (int h = 0; h < 2; ++h)
+        if (i + h > 0) ea = fma2(p.v[i][h], a.v[i][h], ea);
+    const float2 ea2 = up(ea);
+    const float2 sums = up(warp_sum2(pk(row_lane_sum(p), ea2.x + ea2.y)));
+    const float inv = 1.0f / sums.x;
+    const F2 inv2 = both(inv), dot = both(-sums.y * inv);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) a.v[i][c] = p.v[i][c] * (a.v[i][c] - dot);
+      for (int h = 0; h < 2; ++h)
+        a.v[i][h] = mul2(mul2(p.v[i][h], inv2), add2(a.v[i][h], dot));
     row_store<NV, VEC>(a, dlogits + t * E, E, lane);
-    __syncwarp();
-    if (pick >= 0) row[pick] = 0.f;
-    __syncwarp();
   }
 }
 
@@ -355,11 +397,13 @@ static cudaError_t route_backward_typed(const float* logits, const float* offset
   return with_row_shape(E, [&](auto nv, auto vec) {
     constexpr auto kern =
         route_backward_kernel<decltype(nv)::value, decltype(vec)::value != 0, OUT>;
-    const int64_t want = (T + BAL_WARPS - 1) / BAL_WARPS;
+    // one wave of resident blocks, each an equal range of whole warp steps
     const int64_t cap = static_cast<int64_t>(device_sms()) * blocks_per_sm<kern>(BAL_THREADS, smem);
-    return launch_pdl(kern, dim3(static_cast<unsigned>(want < cap ? want : cap)),
+    const int64_t steps = (T + BAL_WARPS - 1) / BAL_WARPS;
+    const int64_t chunk = (steps + cap - 1) / cap * BAL_WARPS;
+    return launch_pdl(kern, dim3(static_cast<unsigned>((T + chunk - 1) / chunk)),
                       dim3(BAL_THREADS), smem, stream, logits, offset, idx, dgate, mask, seq, coef,
-                      dloss, T, S, E, K, dlogits);
+                      dloss, T, S, E, K, static_cast<int>(chunk), dlogits);
   });
 }
 

@@ -1,27 +1,33 @@
 // rows.cuh -- one warp's access to a row of E fp32 logits, shared by the
 // kernels with which the router learns (balance.cu).
 //
-// Lane l owns elements 4 l + 128 i + c (i < NV, c < 4): with E % 4 == 0 (all
-// rows then start on 16 bytes) a row is read and written as 16-byte vectors,
-// 512 contiguous bytes per warp instruction; otherwise element by element
-// with the same ownership.
+// Lane l owns elements 4 l + 128 i + c (i < NV, c < 4), held as pairs: with
+// E % 4 == 0 (all rows then start on 16 bytes) a row is read and written as
+// 16-byte vectors, 512 contiguous bytes per warp instruction; otherwise element
+// by element with the same ownership.
 #pragma once
 
 #include <cfloat>
+#include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
 
-namespace moezc {
+#include "packed.cuh"
 
-constexpr int ROW_MAX_NV = 8;   // 128 * 8 = 1024 logits
+namespace moezc {
 
 template <int NV>
 struct Row {
-  float v[NV][4];
+  F2 v[NV][2];
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i][0] = v[i][1] = both(x);
+  }
 };
 
+// Elements past E read as `fill`.
 template <int NV, bool VEC>
-__device__ __forceinline__ void row_load(Row<NV>& r, const float* __restrict__ src, int E,
+__device__ __forceinline__ void row_load(Row<NV>& r, const float* src, int E,
                                          int lane, float fill) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -29,10 +35,13 @@ __device__ __forceinline__ void row_load(Row<NV>& r, const float* __restrict__ s
     if (VEC) {
       float4 q = make_float4(fill, fill, fill, fill);
       if (j < E) q = *reinterpret_cast<const float4*>(src + j);
-      r.v[i][0] = q.x; r.v[i][1] = q.y; r.v[i][2] = q.z; r.v[i][3] = q.w;
+      r.v[i][0] = pk(q.x, q.y);
+      r.v[i][1] = pk(q.z, q.w);
     } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) r.v[i][c] = j + c < E ? src[j + c] : fill;
+      for (int h = 0; h < 2; ++h)
+        r.v[i][h] = pk(j + 2 * h < E ? src[j + 2 * h] : fill,
+                       j + 2 * h + 1 < E ? src[j + 2 * h + 1] : fill);
     }
   }
 }
@@ -43,14 +52,14 @@ __device__ __forceinline__ void row_store(const Row<NV>& r, float* __restrict__ 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = 4 * lane + 128 * i;
+    const float2 a = up(r.v[i][0]), b = up(r.v[i][1]);
     if (VEC) {
-      if (j < E)
-        *reinterpret_cast<float4*>(dst + j) =
-            make_float4(r.v[i][0], r.v[i][1], r.v[i][2], r.v[i][3]);
+      if (j < E) __stcs(reinterpret_cast<float4*>(dst + j), make_float4(a.x, a.y, b.x, b.y));
     } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (j + c < E) dst[j + c] = r.v[i][c];
+      if (j < E) dst[j] = a.x;
+      if (j + 1 < E) dst[j + 1] = a.y;
+      if (j + 2 < E) dst[j + 2] = b.x;
+      if (j + 3 < E) dst[j + 3] = b.y;
     }
   }
 }
@@ -62,19 +71,17 @@ __device__ __forceinline__ void row_store(const Row<NV>& r, __nv_bfloat16* __res
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = 4 * lane + 128 * i;
+    const __nv_bfloat162 a = __float22bfloat162_rn(up(r.v[i][0]));
+    const __nv_bfloat162 b = __float22bfloat162_rn(up(r.v[i][1]));
     if (VEC) {
-      if (j < E) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(r.v[i][0], r.v[i][1]);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(r.v[i][2], r.v[i][3]);
-        uint2 q;
-        q.x = *reinterpret_cast<const uint32_t*>(&a);
-        q.y = *reinterpret_cast<const uint32_t*>(&b);
-        *reinterpret_cast<uint2*>(dst + j) = q;
-      }
+      if (j < E)
+        __stcs(reinterpret_cast<uint2*>(dst + j), make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                                            *reinterpret_cast<const uint32_t*>(&b)));
     } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (j + c < E) dst[j + c] = __float2bfloat16_rn(r.v[i][c]);
+      if (j < E) dst[j] = a.x;
+      if (j + 1 < E) dst[j + 1] = a.y;
+      if (j + 2 < E) dst[j + 2] = b.x;
+      if (j + 3 < E) dst[j + 3] = b.y;
     }
   }
 }
@@ -84,41 +91,65 @@ __device__ __forceinline__ float warp_sum(float x) {
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+// Two sums at once.
+__device__ __forceinline__ F2 warp_sum2(F2 x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = add2(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_max(float x) {   // (a NaN is passed over)
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
-// Softmax of the row in place (absent elements, loaded as -FLT_MAX, get 0):
-// p = exp(l - max) / sum, fp32.  offset (or nullptr) is added first.
+// The row's exponentials exp(l + offset - max), in place; offset may be
+// nullptr.  Absent elements, loaded as -inf, and logits of -inf become 0; a row
+// of nothing but -inf, or with a NaN or +inf, becomes NaN.  (2 to the power of
+// (l - max) log2 e: 2^-22 and |l - max| 2^-24 relative, far inside the error of
+// the sums taken of them.)
 template <int NV, bool VEC>
-__device__ __forceinline__ void row_softmax(Row<NV>& r, const float* __restrict__ offset, int E,
-                                            int lane) {
+__device__ __forceinline__ void row_exp(Row<NV>& r, const float* __restrict__ offset, int E,
+                                        int lane) {
   if (offset) {
     Row<NV> o;
     row_load<NV, VEC>(o, offset, E, lane, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) r.v[i][c] += o.v[i][c];
+      for (int h = 0; h < 2; ++h) r.v[i][h] = add2(r.v[i][h], o.v[i][h]);
   }
-  float mx = -FLT_MAX;
+  float mx = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) mx = fmaxf(mx, r.v[i][c]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int j = 4 * lane + 128 * i + c;
-      r.v[i][c] = j < E ? expf(r.v[i][c] - mx) : 0.f;
-      sum += r.v[i][c];
+    for (int h = 0; h < 2; ++h) {
+      const float2 a = up(r.v[i][h]);
+      mx = fmaxf(mx, fmaxf(a.x, a.y));
     }
-  const float inv = 1.0f / warp_sum(sum);
+  const F2 neg = both(-warp_max(mx)), log2e = both(1.4426950408889634f);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) r.v[i][c] *= inv;
+    for (int h = 0; h < 2; ++h) {
+      const float2 x = up(mul2(add2(r.v[i][h], neg), log2e));
+      r.v[i][h] = pk(ex2_approx(x.x), ex2_approx(x.y));
+    }
+}
+
+// This lane's part of a row's sum.
+template <int NV>
+__device__ __forceinline__ float row_lane_sum(const Row<NV>& r) {
+  F2 s = add2(r.v[0][0], r.v[0][1]);
+#pragma unroll
+  for (int i = 1; i < NV; ++i) s = add2(s, add2(r.v[i][0], r.v[i][1]));
+  const float2 a = up(s);
+  return a.x + a.y;
 }
 
 // Calls f with integral constants (vectors per lane, whether rows are read as
