@@ -446,11 +446,23 @@ cudaError_t launch_some(const AdamTensor* t, int nt, bool advance, const AdamHyp
   a.lr_scale = lr_scale;
   a.grad_scale = grad_scale;
   const int64_t grid = units < cap ? (units > 0 ? units : 1) : cap;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(Y::THREADS), 0, stream, a);
+  // (launch_pdl's launch, with the parameters taken where they are)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(Y::THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* params[1] = {&a};
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kern), params);
 }
 
 // Tensors of one launch: as many as its parameters (32764 bytes at most) hold.
-constexpr int ADAM_FEW = 16, ADAM_MANY = 448;
+// (The driver copies all of them whatever a launch uses: fewer for fewer tensors.)
+constexpr int ADAM_FEW = 16, ADAM_SOME = 80, ADAM_MANY = 448;
 static_assert(sizeof(AdamArgs<ADAM_MANY>) <= 32764, "kernel parameters");
 
 template <typename Y>
@@ -458,6 +470,8 @@ cudaError_t launch_all(const AdamTensor* t, int nt, const AdamHyper& h, int* ste
                        const float* lr_scale, const float* grad_scale, cudaStream_t stream) {
   if (nt <= ADAM_FEW)
     return launch_some<Y, ADAM_FEW>(t, nt, true, h, step, lr_scale, grad_scale, stream);
+  if (nt <= ADAM_SOME)
+    return launch_some<Y, ADAM_SOME>(t, nt, true, h, step, lr_scale, grad_scale, stream);
   for (int i = 0; i < nt; i += ADAM_MANY) {
     const int k = nt - i < ADAM_MANY ? nt - i : ADAM_MANY;
     const cudaError_t e = launch_some<Y, ADAM_MANY>(t + i, k, i + k == nt, h, step, lr_scale,

@@ -7,7 +7,6 @@ the call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional, Sequence
@@ -351,28 +350,50 @@ def combine(x: torch.Tensor, y_rows: torch.Tensor, slot: torch.Tensor, gate: tor
     return out
 
 
+# Handle of a device's current stream (torch.cuda.current_stream builds a Stream
+# object for it, 3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _on(stream):
     """Context in which what a call allocates belongs to the stream it runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)))
     return torch.cuda.stream(stream)
 
 
-def _arg(t: Optional[torch.Tensor], dtype, shape, name: str) -> Optional[int]:
-    """Address of a contiguous tensor of this type and shape on the current device."""
+def _empty(stream, dev, *specs):
+    """Uninitialised tensors of the given (shape, dtype) on the call's stream."""
+    if stream is None:
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
+    with _on(stream):
+        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
+
+
+def _arg(t: Optional[torch.Tensor], dtype, shape, name: str, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor of this type and shape on CUDA device dev,
+    the current one."""
     if t is None:
         return None
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and dev >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+def _stream_of(stream, dev: int) -> int:
+    return _raw_stream(dev) if stream is None else _stream_ptr(stream)
 
 
 def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: torch.Tensor, N: int, Z: int, K: int,
@@ -382,17 +403,14 @@ def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: torch.Tensor, N: int, Z:
     T, d = x.shape
     E = N + Z
     f32, bf, i32 = torch.float32, torch.bfloat16, torch.int32
-    args = (_arg(x, bf, (T, d), "x"), _arg(W_r, bf, (E, d), "W_r"), _arg(b, f32, (E,), "b"),
-            _arg(logit_offset, f32, (E,), "logit_offset"))
-    with _on(stream):
-        logits = torch.empty(T, E, dtype=f32, device=x.device)
-        idx = torch.empty(T, K, dtype=i32, device=x.device)
-        gate = torch.empty(T, K, dtype=f32, device=x.device)
-        zsum = torch.empty(T, dtype=f32, device=x.device)
-        counts = torch.empty(E, dtype=i32, device=x.device)
+    dev = _current_device()
+    args = (_arg(x, bf, (T, d), "x", dev), _arg(W_r, bf, (E, d), "W_r", dev),
+            _arg(b, f32, (E,), "b", dev), _arg(logit_offset, f32, (E,), "logit_offset", dev))
+    logits, idx, gate, zsum, counts = _empty(stream, x.device, ((T, E), f32), ((T, K), i32),
+                                             ((T, K), f32), ((T,), f32), ((E,), i32))
     _check(lib().moe_zc_route_logits(*args, T, d, N, Z, K, logits.data_ptr(), idx.data_ptr(),
                                      gate.data_ptr(), zsum.data_ptr(), counts.data_ptr(),
-                                     _stream_ptr(stream)), "moe_zc_route_logits")
+                                     _stream_of(stream, dev)), "moe_zc_route_logits")
     return logits, idx, gate, zsum, counts
 
 
@@ -404,21 +422,22 @@ class BalanceLoss(NamedTuple):
     coef: torch.Tensor      # fp32 [S, E]: d loss_s / d p_{t,i}, for route_backward
 
 
-def _row_args(logits, idx, logit_offset, mask, seq_start):
-    """Addresses and sizes that balance_loss and route_backward share."""
+def _row_args(logits, idx, logit_offset, mask, seq_start, dev):
+    """Sizes and addresses that balance_loss and route_backward share."""
     T, E = logits.shape
     K = idx.shape[1] if idx is not None else 1
     S = seq_start.numel() - 1 if seq_start is not None else 1
     if S < 0:
         raise ValueError("seq_start holds one offset more than there are sequences")
-    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
-        raise ValueError(f"mask must be torch.bool or torch.uint8, got {mask.dtype}")
-    return T, E, K, S, (
-        _arg(logits, torch.float32, (T, E), "logits"),
-        _arg(logit_offset, torch.float32, (E,), "logit_offset"),
-        _arg(idx, torch.int32, (T, K), "idx"),
-        _arg(mask, mask.dtype, (T,), "mask") if mask is not None else None,
-        _arg(seq_start, torch.int32, (S + 1,), "seq_start"))
+    mp = None
+    if mask is not None:
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"mask must be torch.bool or torch.uint8, got {mask.dtype}")
+        mp = _arg(mask, mask.dtype, (T,), "mask", dev)
+    return (T, E, K, S, _arg(logits, torch.float32, (T, E), "logits", dev),
+            _arg(logit_offset, torch.float32, (E,), "logit_offset", dev),
+            _arg(idx, torch.int32, (T, K), "idx", dev), mp,
+            _arg(seq_start, torch.int32, (S + 1,), "seq_start", dev))
 
 
 def balance_loss(logits: torch.Tensor, idx: torch.Tensor,
@@ -432,23 +451,23 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor,
     (bool or uint8 [T]) drops padding tokens; seq_start (int32 [S + 1]) holds
     the sequences' offsets (None: one sequence); weight (fp32 [E]) the inverse
     target shares (None: an even load)."""
-    T, E, K, S, (lp, op, ip, mp, sp) = _row_args(logits, idx, logit_offset, mask, seq_start)
-    wp = _arg(weight, torch.float32, (E,), "weight")
+    dev = _current_device()
+    T, E, K, S, lp, op, ip, mp, sp = _row_args(logits, idx, logit_offset, mask, seq_start, dev)
+    wp = _arg(weight, torch.float32, (E,), "weight", dev)
     nbytes = ctypes.c_int64(0)
-    _check(lib().moe_zc_balance_workspace(T, S, E, ctypes.byref(nbytes)),
-           "moe_zc_balance_workspace")
-    dev, f32 = logits.device, torch.float32
-    with _on(stream):
-        r = BalanceLoss(torch.empty(S, dtype=f32, device=dev),
-                        torch.empty(S, E, dtype=torch.int32, device=dev),
-                        torch.empty(S, E, dtype=f32, device=dev),
-                        torch.empty(S, E, dtype=f32, device=dev))
-        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=dev)
-    _check(lib().moe_zc_balance_loss(lp, op, ip, mp, sp, wp, T, S, E, K, r.loss.data_ptr(),
-                                     r.counts.data_ptr(), r.prob.data_ptr(), r.coef.data_ptr(),
-                                     ws.data_ptr(), nbytes.value, _stream_ptr(stream)),
+    L = lib()
+    _check(L.moe_zc_balance_workspace(T, S, E, ctypes.byref(nbytes)), "moe_zc_balance_workspace")
+    f32 = torch.float32
+    # (coef first: it is the one that has to be 16-byte aligned)
+    table, loss, ws = _empty(stream, logits.device, ((3, S, E), f32), ((S,), f32),
+                             ((nbytes.value,), torch.uint8))
+    coef, prob, counts = table.unbind(0)
+    counts = counts.view(torch.int32)
+    _check(L.moe_zc_balance_loss(lp, op, ip, mp, sp, wp, T, S, E, K, loss.data_ptr(),
+                                 counts.data_ptr(), prob.data_ptr(), coef.data_ptr(),
+                                 ws.data_ptr(), nbytes.value, _stream_of(stream, dev)),
            "moe_zc_balance_loss")
-    return r
+    return BalanceLoss(loss, counts, prob, coef)
 
 
 def route_backward(logits: torch.Tensor, idx: Optional[torch.Tensor] = None,
@@ -461,23 +480,24 @@ def route_backward(logits: torch.Tensor, idx: Optional[torch.Tensor] = None,
     the gates' gradient dgate (fp32 [T, K], with idx) and/or the balance loss's
     (coef from balance_loss, dloss fp32 [S] the gradient of each loss_s).
     Masked tokens get zeros."""
-    if dtype not in (torch.float32, torch.bfloat16):
+    f32 = torch.float32
+    if dtype is not f32 and dtype is not torch.bfloat16:
         raise ValueError(f"dtype must be torch.float32 or torch.bfloat16, got {dtype}")
     if dgate is not None and idx is None:
         raise ValueError("dgate needs idx")
     if (coef is None) != (dloss is None):
         raise ValueError("coef and dloss go together")
-    T, E, K, S, (lp, op, ip, mp, sp) = _row_args(logits, idx, logit_offset, mask, seq_start)
-    gp = _arg(dgate, torch.float32, (T, K), "dgate")
-    cp = _arg(coef, torch.float32, (S, E), "coef")
-    dp = _arg(dloss, torch.float32, (S,), "dloss")
-    with _on(stream):
-        out = torch.empty(T, E, dtype=dtype, device=logits.device)
+    dev = _current_device()
+    T, E, K, S, lp, op, ip, mp, sp = _row_args(logits, idx, logit_offset, mask, seq_start, dev)
+    gp = _arg(dgate, f32, (T, K), "dgate", dev)
+    cp = _arg(coef, f32, (S, E), "coef", dev)
+    dp = _arg(dloss, f32, (S,), "dloss", dev)
+    (out,) = _empty(stream, logits.device, ((T, E), dtype))
     if S == 0:
         cp = dp = None   # no sequence, no loss
     _check(lib().moe_zc_route_backward(lp, op, ip, gp, mp, sp, cp, dp, T, S, E, K, out.data_ptr(),
-                                       BF16 if dtype == torch.bfloat16 else F32,
-                                       _stream_ptr(stream)), "moe_zc_route_backward")
+                                       F32 if dtype is f32 else BF16, _stream_of(stream, dev)),
+           "moe_zc_route_backward")
     return out
 
 
@@ -488,16 +508,18 @@ def combine_backward(dout: torch.Tensor, x: torch.Tensor, y_rows: torch.Tensor,
     T, d = dout.shape
     K = slot.shape[1]
     R = y_rows.shape[0]
-    bf = torch.bfloat16
-    args = (_arg(dout, bf, (T, d), "dout"), _arg(x, bf, (T, d), "x"),
-            _arg(y_rows, bf, (R, d), "y_rows"), _arg(slot, torch.int32, (T, K), "slot"),
-            _arg(gate, torch.float32, (T, K), "gate"))
-    with _on(stream):
-        dgate = torch.empty(T, K, dtype=torch.float32, device=dout.device)
-        dy = torch.empty_like(y_rows) if rows else None
+    bf, f32 = torch.bfloat16, torch.float32
+    dev = _current_device()
+    args = (_arg(dout, bf, (T, d), "dout", dev), _arg(x, bf, (T, d), "x", dev),
+            _arg(y_rows, bf, (R, d), "y_rows", dev), _arg(slot, torch.int32, (T, K), "slot", dev),
+            _arg(gate, f32, (T, K), "gate", dev))
+    if rows:
+        dgate, dy = _empty(stream, dout.device, ((T, K), f32), ((R, d), bf))
+    else:
+        (dgate,), dy = _empty(stream, dout.device, ((T, K), f32)), None
     _check(lib().moe_zc_combine_backward(*args, T, d, K, R, dgate.data_ptr(),
-                                         dy.data_ptr() if rows else None, _stream_ptr(stream)),
-           "moe_zc_combine_backward")
+                                         dy.data_ptr() if rows else None,
+                                         _stream_of(stream, dev)), "moe_zc_combine_backward")
     return dgate, dy
 
 
@@ -547,30 +569,32 @@ class AdamW:
             v = getattr(self, name)
             if v is not None and len(v) != len(self.params):
                 raise ValueError(f"{name} must hold one entry per parameter")
+        self._shapes = [p.shape for p in self.params]
+        n = [p.numel() for p in self.params]
         self._table = np.zeros(len(self.params), dtype=_ADAMW_TENSOR)
-        spans = []
+        self._table["n"] = n
+        dev = p0.get_device()
+        spans = []   # what the step writes
 
-        def put(i, field, t, dtype, shape, name):
-            if t.device != self.device:
-                raise ValueError(f"{name}[{i}] must be on {self.device}")
-            self._table[field][i] = _arg(t, dtype, shape, f"{name}[{i}]")
-            if t.numel():
-                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
+        def put(field, tensors, dtype, shapes, name):
+            ptrs = []
+            for i, (t, shape) in enumerate(zip(tensors, shapes)):
+                ptrs.append(_arg(t, dtype, shape, (name, i), dev))
+                spans.append((ptrs[-1], ptrs[-1] + t.numel() * t.element_size()))
+            self._table[field] = ptrs
 
-        for i, p in enumerate(self.params):
-            n = p.numel()
-            self._table["n"][i] = n
-            put(i, "param", p, p0.dtype, p.shape, "params")
-            for field, v in (("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)):
-                if eight:
-                    put(i, field, v[i].codes, torch.uint8, p.shape, field)
-                    put(i, field + "_scale", v[i].scales, torch.float32,
-                        (-(-n // ADAMW_BLOCK),), field + " scales")
-                else:
-                    put(i, field, v[i], torch.float32, p.shape, field)
-            if self.master is not None:
-                put(i, "master", self.master[i], torch.float32, p.shape, "master")
-        spans.sort()
+        put("param", self.params, p0.dtype, self._shapes, "params")
+        for field in ("exp_avg", "exp_avg_sq"):
+            v = getattr(self, field)
+            if eight:
+                put(field, [q.codes for q in v], torch.uint8, self._shapes, field)
+                put(field + "_scale", [q.scales for q in v], torch.float32,
+                    [(-(-k // ADAMW_BLOCK),) for k in n], field + " scales")
+            else:
+                put(field, v, torch.float32, self._shapes, field)
+        if self.master is not None:
+            put("master", self.master, torch.float32, self._shapes, "master")
+        spans = sorted(q for q in spans if q[0] < q[1])
         for (_, end), (start, _) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError("params and states must not overlap")
@@ -598,22 +622,21 @@ class AdamW:
         gt = grads[0].dtype
         if gt not in (torch.float32, torch.bfloat16):
             raise ValueError(f"grads must be torch.float32 or torch.bfloat16, got {gt}")
-        dev = self.device
-        if dev.index != torch.cuda.current_device():
-            raise ValueError(f"the current CUDA device must be {dev}")
-        ptrs = []
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            if g.dtype != gt or g.shape != p.shape or g.device != dev or not g.is_contiguous():
+        dev = _current_device()
+        if self.device.index != dev:
+            raise ValueError(f"the current CUDA device must be {self.device}")
+        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+            if (g.dtype is not gt or g.shape != shape or g.get_device() != dev
+                    or not g.is_contiguous()):
                 raise ValueError(f"grads[{i}] must be a contiguous {gt} tensor of shape "
-                                 f"{tuple(p.shape)} on {dev}")
-            ptrs.append(g.data_ptr())
-        self._table["grad"] = ptrs
+                                 f"{tuple(shape)} on {self.device}")
+        self._table["grad"] = [g.data_ptr() for g in grads]
         self.args.grad_type = BF16 if gt == torch.bfloat16 else F32
-        scales = [None if t is None else _arg(t.view(-1), torch.float32, (1,), name)
+        scales = [None if t is None else _arg(t.view(-1), torch.float32, (1,), name, dev)
                   for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale"))]
-        st = _stream_ptr(stream)
-        _check(lib().moe_zc_adamw(self._table.ctypes.data, len(ptrs), ctypes.byref(self.args),
-                                  self.step_count.data_ptr(), *scales, st), "moe_zc_adamw")
+        _check(lib().moe_zc_adamw(self._table.ctypes.data, len(grads), ctypes.byref(self.args),
+                                  self.step_count.data_ptr(), *scales, _stream_of(stream, dev)),
+               "moe_zc_adamw")
 
 
 def forward_host(x_host: torch.Tensor, W_r: torch.Tensor, b: torch.Tensor,
