@@ -71,24 +71,47 @@ __device__ __forceinline__ int seq_of(const int* __restrict__ seq, int S, int64_
   return lo;
 }
 
+// Which of a warp's next 32 tokens (t, t + BAL_WARPS, ... below end) are not
+// masked, as bits.
+__device__ __forceinline__ unsigned on_bits(const uint8_t* __restrict__ mask, int64_t t,
+                                            int64_t end, int lane) {
+  const int64_t u = t + static_cast<int64_t>(lane) * BAL_WARPS;
+  return __ballot_sync(0xffffffffu, !mask || (u < end && mask[u]));
+}
+
 // Partial sums of one (block, sequence) pair: block b's tokens of sequence s
 // go to slot b + s.  Walking the tokens, each step ends a block or a sequence,
-// so no two pairs share a slot and blocks + sequences slots are enough.
+// so no two pairs share a slot and blocks + sequences slots are enough.  Warp w
+// takes tokens w, w + BAL_WARPS, ... of the block's range.
 template <int NV, bool VEC>
-__global__ void __launch_bounds__(BAL_THREADS)
+__global__ void __launch_bounds__(BAL_THREADS, 2)
 balance_partial_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                        const int* __restrict__ idx, const uint8_t* __restrict__ mask,
                        const int* __restrict__ seq, int64_t T, int S, int E, int K, int chunk,
                        float* __restrict__ psum, int* __restrict__ pcnt, int* __restrict__ pn) {
+  using Ring = RowRing<NV, VEC>;
   extern __shared__ __align__(16) float smem_f[];
-  float* red = smem_f;                                         // [BAL_WARPS][E]
-  int* hist = reinterpret_cast<int*>(smem_f + BAL_WARPS * E);  // [E]
+  float* red = smem_f + BAL_WARPS * (Ring::BYTES / 4);          // [BAL_WARPS][E]
+  int* hist = reinterpret_cast<int*>(red + BAL_WARPS * E);      // [E]
   __shared__ int nvalid[BAL_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
+  Ring ring{smem_f + warp * (Ring::BYTES / 4)};
+  int64_t f = t0 + warp;
+  auto fetch = [&]() {
+    if (f < t1)
+      ring.fetch(logits + f * E, idx + f * K, nullptr, E, K, lane);
+    else
+      ring.none();
+    f += BAL_WARPS;
+  };
+  for (int i = 0; i < Ring::DEPTH - 1; ++i) fetch();
+  int64_t u = t0 + warp;      // this warp's next token
+  unsigned on = 0;            // the mask of its next ones
+  int left = 0;               // ... how many bits of it are still ahead
   int64_t t = t0;
   for (int s = seq_of(seq, S, t0, T, lane); s < S && t < t1; ++s) {
     const int64_t sa = seq_at(seq, s, T), se = seq_at(seq, s + 1, T);
@@ -100,30 +123,27 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
     Row<NV> acc;
     acc.fill(0.f);
     int n = 0;
-    // the next token's row is on its way while this one is summed
-    Row<NV> nxt;
-    int nxt_pick = -1;
-    bool nxt_on = true;
-    auto fetch = [&](int64_t u) {
-      if (u >= e) return;
-      row_load<NV, VEC>(nxt, logits + u * E, E, lane, -INFINITY);
-      nxt_pick = lane < K ? idx[u * K + lane] : -1;
-      nxt_on = !mask || mask[u];
-    };
-    fetch(a + warp);
-    for (int64_t u = a + warp; u < e; u += BAL_WARPS) {
-      Row<NV> r = nxt;
-      const int pick = nxt_pick;
-      const bool on = nxt_on;
-      fetch(u + BAL_WARPS);
-      if (!on) continue;
+    for (; u < e; u += BAL_WARPS) {
+      if (left == 0) {
+        on = on_bits(mask, u, t1, lane);
+        left = 32;
+      }
+      const bool counts = u >= a && (on & 1u);   // (tokens in a gap before a are passed over)
+      on >>= 1;
+      --left;
+      fetch();
+      Row<NV> r;
+      int pick;
+      float none;
+      ring.take(r, pick, none, E, lane);
+      if (!counts) continue;
       row_exp<NV, VEC>(r, offset, E, lane);
       const F2 inv = both(1.0f / warp_sum(row_lane_sum(r)));
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) acc.v[i][h] = fma2(r.v[i][h], inv, acc.v[i][h]);
-      if (pick >= 0 && pick < E) atomicAdd(&hist[pick], 1);
+      if (lane < K && pick >= 0 && pick < E) atomicAdd(&hist[pick], 1);
       ++n;
     }
     row_put<NV, VEC>(acc, red + warp * E, E, lane);
@@ -146,6 +166,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
     __syncthreads();
     t = e;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Partial sums added up: a cluster of CTAs per sequence (one wherever E <= 128),
@@ -167,9 +188,10 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
   __shared__ float cta_part[8];      // (first CTA) the CTAs' parts
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int s = blockIdx.x / nc, rank = blockIdx.x % nc;
+  // (seq was complete before the partial sums' kernel let this one start)
+  const int64_t a = seq_at(seq, s, T), e = seq_at(seq, s + 1, T);
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t a = seq_at(seq, s, T), e = seq_at(seq, s + 1, T);
   const int64_t b0 = a / chunk, b1 = a < e ? (e - 1) / chunk + 1 : b0;
   const int64_t r0 = b0 + s, rows = b1 - b0;     // this sequence's slots
   const int j0 = rank * 128 + 4 * x;
@@ -243,45 +265,46 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
 // only at a boundary.  The picks' dgate are added into a row of shared memory
 // per warp (zero between tokens).
 template <int NV, bool VEC, typename OUT>
-__global__ void __launch_bounds__(BAL_THREADS)
+__global__ void __launch_bounds__(BAL_THREADS, 2)
 route_backward_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                       const int* __restrict__ idx, const float* __restrict__ dgate,
                       const uint8_t* __restrict__ mask, const int* __restrict__ seq,
                       const float* __restrict__ coef, const float* __restrict__ dloss, int64_t T,
                       int S, int E, int K, int chunk, OUT* __restrict__ dlogits) {
+  using Ring = RowRing<NV, VEC>;
   extern __shared__ __align__(16) float smem_f[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* row = smem_f + warp * ((E + 3) & ~3);
+  float* row = smem_f + BAL_WARPS * (Ring::BYTES / 4) + warp * ((E + 3) & ~3);
   for (int j = lane; j < E; j += 32) row[j] = 0.f;
   __syncwarp();
   griddep_wait();
   griddep_launch_dependents();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
-  // the next token's row is on its way while this one is worked on
-  Row<NV> nxt;
-  int nxt_pick = -1;
-  float nxt_g = 0.f;
-  bool nxt_on = true;
-  auto fetch = [&](int64_t t) {
-    if (t >= t1) return;
-    row_load<NV, VEC>(nxt, logits + t * E, E, lane, -INFINITY);
-    nxt_on = !mask || mask[t];
-    if (dgate && lane < K) {
-      nxt_pick = idx[t * K + lane];
-      nxt_g = dgate[t * K + lane];
-    }
+  Ring ring{smem_f + warp * (Ring::BYTES / 4)};
+  int64_t f = t0 + warp;
+  auto fetch = [&]() {
+    if (f < t1)
+      ring.fetch(logits + f * E, dgate ? idx + f * K : nullptr, dgate ? dgate + f * K : nullptr, E,
+                 K, lane);
+    else
+      ring.none();
+    f += BAL_WARPS;
   };
-  fetch(t0 + warp);
+  for (int i = 0; i < Ring::DEPTH - 1; ++i) fetch();
   // tokens [sa, se) share s (S: no sequence); none known yet
   int s = S;
   int64_t sa = 0, se = coef ? 0 : T;
+  unsigned bits = 0;
+  int left = 0;
   for (int64_t t = t0 + warp; t < t1; t += BAL_WARPS) {
-    Row<NV> p = nxt;
-    int pick = nxt_pick;
-    const float g = nxt_g;
-    const bool on = nxt_on;
-    fetch(t + BAL_WARPS);
+    if (left == 0) {
+      bits = on_bits(mask, t, t1, lane);
+      left = 32;
+    }
+    const bool on = bits & 1u;
+    bits >>= 1;
+    --left;
     if (t < sa || t >= se) {
       s = seq_of(seq, S, t, T, lane);
       sa = s < S ? seq_at(seq, s, T) : t;
@@ -292,6 +315,12 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         s = S;
       }
     }
+    fetch();
+    Row<NV> p;
+    int pick;
+    float g;
+    ring.take(p, pick, g, E, lane);
+    if (lane >= K) pick = -1;
     Row<NV> a;
     if (!on || (!dgate && s >= S)) {
       // no gradient reaches this token (whatever its logits hold)
@@ -349,6 +378,7 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         a.v[i][h] = mul2(mul2(p.v[i][h], inv2), add2(a.v[i][h], dot));
     row_store<NV, VEC>(a, dlogits + t * E, E, lane);
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 }  // namespace
@@ -364,9 +394,14 @@ cudaError_t launch_balance_loss(const float* logits, const float* offset, const 
   int* pcnt = reinterpret_cast<int*>(ws + pl.cnt_off);
   int* pn = reinterpret_cast<int*>(ws + pl.n_off);
   if (pl.blocks > 0) {
-    const size_t smem = static_cast<size_t>(BAL_WARPS + 1) * E * sizeof(float);
     const cudaError_t e = with_row_shape(E, [&](auto nv, auto vec) {
-      constexpr auto kern = balance_partial_kernel<decltype(nv)::value, decltype(vec)::value != 0>;
+      constexpr int NV = decltype(nv)::value;
+      constexpr bool VEC = decltype(vec)::value != 0;
+      constexpr auto kern = balance_partial_kernel<NV, VEC>;
+      constexpr int ring = BAL_WARPS * RowRing<NV, VEC>::BYTES;
+      const size_t smem = ring + static_cast<size_t>(BAL_WARPS + 1) * E * sizeof(float);
+      const cudaError_t el = smem_limit<kern>(ring + (BAL_WARPS + 1) * NV * 512);
+      if (el != cudaSuccess) return el;
       return launch_pdl(kern, dim3(static_cast<unsigned>(pl.blocks)), dim3(BAL_THREADS), smem,
                         stream, logits, offset, idx, mask, seq, T, S, E, K, pl.chunk, psum, pcnt,
                         pn);
@@ -393,10 +428,15 @@ static cudaError_t route_backward_typed(const float* logits, const float* offset
                                         const float* dgate, const uint8_t* mask, const int* seq,
                                         const float* coef, const float* dloss, int64_t T, int S,
                                         int E, int K, OUT* dlogits, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(BAL_WARPS) * ((E + 3) & ~3) * sizeof(float);
   return with_row_shape(E, [&](auto nv, auto vec) {
-    constexpr auto kern =
-        route_backward_kernel<decltype(nv)::value, decltype(vec)::value != 0, OUT>;
+    constexpr int NV = decltype(nv)::value;
+    constexpr bool VEC = decltype(vec)::value != 0;
+    constexpr auto kern = route_backward_kernel<NV, VEC, OUT>;
+    // (the same shared memory for every E of the shape, so that the occupancy
+    // looked up once holds for all of them)
+    constexpr int smem = BAL_WARPS * (RowRing<NV, VEC>::BYTES + NV * 512);
+    const cudaError_t el = smem_limit<kern>(smem);
+    if (el != cudaSuccess) return el;
     // one wave of resident blocks, each an equal range of whole warp steps
     const int64_t cap = static_cast<int64_t>(device_sms()) * blocks_per_sm<kern>(BAL_THREADS, smem);
     const int64_t steps = (T + BAL_WARPS - 1) / BAL_WARPS;

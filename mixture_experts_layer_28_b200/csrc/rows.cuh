@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 
 #include "packed.cuh"
+#include "ptx.cuh"
 
 namespace moezc {
 
@@ -151,6 +152,77 @@ __device__ __forceinline__ float row_lane_sum(const Row<NV>& r) {
   const float2 a = up(s);
   return a.x + a.y;
 }
+
+// A warp's rows on their way to it: a ring of DEPTH stages in shared memory,
+// each a row and two arrays of up to 32 words, filled by asynchronous copies.
+// Each lane reads back only what it copied itself, so waiting for its own
+// copies is all the ordering there is, and DEPTH - 1 tokens are in flight
+// without holding registers (a single row ahead in registers left each token
+// waiting for most of a memory latency).
+template <int NV, bool VEC>
+struct RowRing {
+  static constexpr int WORDS = NV * 128 + 64;       // of a stage
+  static constexpr int DEPTH = NV >= 8 ? 2 : NV >= 6 ? 3 : NV >= 4 ? 4 : NV >= 3 ? 5 : 6;
+  static constexpr int BYTES = DEPTH * WORDS * 4;   // per warp
+  float* base;
+  int put = 0, got = 0;   // stages of the next fetch and the next wait
+
+  static __device__ __forceinline__ void copy4(float* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
+                 : "memory");
+  }
+  // The row at src and, per lane < K, words of a and b (nullptr: none).  One
+  // call a token (or `none`), in order.
+  __device__ __forceinline__ void fetch(const float* src, const int* a, const float* b, int E,
+                                        int K, int lane) {
+    float* st = base + put * WORDS;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = 4 * lane + 128 * i;
+      if (VEC) {
+        if (j < E)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(st + j)),
+                       "l"(src + j)
+                       : "memory");
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (j + c < E) copy4(st + j + c, src + j + c);
+      }
+    }
+    if (lane < K) {
+      if (a) copy4(st + NV * 128 + lane, a + lane);
+      if (b) copy4(st + NV * 128 + 32 + lane, b + lane);
+    }
+    none();
+  }
+  __device__ __forceinline__ void none() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    put = put + 1 == DEPTH ? 0 : put + 1;
+  }
+  // Waits for the oldest token fetched, DEPTH - 1 others staying in flight, and
+  // takes it: its row, and this lane's words.
+  __device__ __forceinline__ void take(Row<NV>& r, int& a, float& b, int E, int lane) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    const float* st = base + got * WORDS;
+    row_load<NV, true>(r, st, VEC ? E : NV * 128, lane, -INFINITY);
+    if (!VEC) row_cut(r, E, lane);
+    a = reinterpret_cast<const int*>(st)[NV * 128 + lane];
+    b = st[NV * 128 + 32 + lane];
+    got = got + 1 == DEPTH ? 0 : got + 1;
+  }
+  // -inf past E, where a vector of four may cross it
+  static __device__ __forceinline__ void row_cut(Row<NV>& r, int E, int lane) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 4 * lane + 128 * i + 2 * h;
+        const float2 a = up(r.v[i][h]);
+        r.v[i][h] = pk(j < E ? a.x : -INFINITY, j + 1 < E ? a.y : -INFINITY);
+      }
+  }
+};
 
 // Calls f with integral constants (vectors per lane, whether rows are read as
 // 16-byte vectors) for rows of E elements.
