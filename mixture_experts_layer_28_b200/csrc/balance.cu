@@ -35,19 +35,19 @@ __device__ __forceinline__ int64_t seq_at(const int* __restrict__ seq, int s, in
 }
 
 // A row into shared memory (E % 4 == 0: 16-byte aligned rows).
-template <int NV, bool VEC>
+template <int NV, int KIND>
 __device__ __forceinline__ void row_put(const Row<NV>& r, float* dst, int E, int lane) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = 4 * lane + 128 * i;
     const float2 a = up(r.v[i][0]), b = up(r.v[i][1]);
-    if (VEC) {
-      if (j < E) *reinterpret_cast<float4*>(dst + j) = make_float4(a.x, a.y, b.x, b.y);
-    } else {
-      if (j < E) dst[j] = a.x;
-      if (j + 1 < E) dst[j + 1] = a.y;
-      if (j + 2 < E) dst[j + 2] = b.x;
-      if (j + 3 < E) dst[j + 3] = b.y;
+    if (KIND == ROW_ODD) {
+      const float f[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (j + c < E) dst[j + c] = f[c];
+    } else if (KIND == ROW_WHOLE || j < E) {
+      *reinterpret_cast<float4*>(dst + j) = make_float4(a.x, a.y, b.x, b.y);
     }
   }
 }
@@ -83,13 +83,13 @@ __device__ __forceinline__ unsigned on_bits(const uint8_t* __restrict__ mask, in
 // go to slot b + s.  Walking the tokens, each step ends a block or a sequence,
 // so no two pairs share a slot and blocks + sequences slots are enough.  Warp w
 // takes tokens w, w + BAL_WARPS, ... of the block's range.
-template <int NV, bool VEC>
+template <int NV, int KIND>
 __global__ void __launch_bounds__(BAL_THREADS, 2)
 balance_partial_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                        const int* __restrict__ idx, const uint8_t* __restrict__ mask,
                        const int* __restrict__ seq, int64_t T, int S, int E, int K, int chunk,
                        float* __restrict__ psum, int* __restrict__ pcnt, int* __restrict__ pn) {
-  using Ring = RowRing<NV, VEC>;
+  using Ring = RowRing<NV, KIND>;
   extern __shared__ __align__(16) float smem_f[];
   float* red = smem_f + BAL_WARPS * (Ring::BYTES / 4);          // [BAL_WARPS][E]
   int* hist = reinterpret_cast<int*>(red + BAL_WARPS * E);      // [E]
@@ -99,7 +99,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
   griddep_launch_dependents();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
-  Ring ring{smem_f + warp * (Ring::BYTES / 4)};
+  Ring ring(smem_f + warp * (Ring::BYTES / 4), lane);
   int64_t f = t0 + warp;
   auto fetch = [&]() {
     if (f < t1)
@@ -137,8 +137,8 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
       float none;
       ring.take(r, pick, none, E, lane);
       if (!counts) continue;
-      row_exp<NV, VEC>(r, offset, E, lane);
-      const F2 inv = both(1.0f / warp_sum(row_lane_sum(r)));
+      row_exp<NV, KIND>(r, offset, E, lane);
+      const F2 inv = both(rcp_approx(warp_sum(row_lane_sum(r))));
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -146,7 +146,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
       if (lane < K && pick >= 0 && pick < E) atomicAdd(&hist[pick], 1);
       ++n;
     }
-    row_put<NV, VEC>(acc, red + warp * E, E, lane);
+    row_put<NV, KIND>(acc, red + warp * E, E, lane);
     if (lane == 0) nvalid[warp] = n;
     __syncthreads();
     const int64_t at = (static_cast<int64_t>(blockIdx.x) + s) * E;
@@ -166,7 +166,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
     __syncthreads();
     t = e;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  ring.drain();
 }
 
 // Partial sums added up: a cluster of CTAs per sequence (one wherever E <= 128),
@@ -264,14 +264,14 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
 // consecutive tokens, so that a warp finds its sequence once and then again
 // only at a boundary.  The picks' dgate are added into a row of shared memory
 // per warp (zero between tokens).
-template <int NV, bool VEC, typename OUT>
+template <int NV, int KIND, typename OUT>
 __global__ void __launch_bounds__(BAL_THREADS, 2)
 route_backward_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                       const int* __restrict__ idx, const float* __restrict__ dgate,
                       const uint8_t* __restrict__ mask, const int* __restrict__ seq,
                       const float* __restrict__ coef, const float* __restrict__ dloss, int64_t T,
                       int S, int E, int K, int chunk, OUT* __restrict__ dlogits) {
-  using Ring = RowRing<NV, VEC>;
+  using Ring = RowRing<NV, KIND>;
   extern __shared__ __align__(16) float smem_f[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* row = smem_f + BAL_WARPS * (Ring::BYTES / 4) + warp * ((E + 3) & ~3);
@@ -281,7 +281,7 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
   griddep_launch_dependents();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
   const int64_t t1 = t0 + chunk < T ? t0 + chunk : T;
-  Ring ring{smem_f + warp * (Ring::BYTES / 4)};
+  Ring ring(smem_f + warp * (Ring::BYTES / 4), lane);
   int64_t f = t0 + warp;
   auto fetch = [&]() {
     if (f < t1)
@@ -295,6 +295,8 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
   // tokens [sa, se) share s (S: no sequence); none known yet
   int s = S;
   int64_t sa = 0, se = coef ? 0 : T;
+  Row<NV> dc;        // dloss_s coef_s of the sequence (0: none)
+  dc.fill(0.f);
   unsigned bits = 0;
   int left = 0;
   for (int64_t t = t0 + warp; t < t1; t += BAL_WARPS) {
@@ -314,6 +316,15 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         sa = t;
         s = S;
       }
+      dc.fill(0.f);
+      if (s < S) {
+        row_load<NV, KIND>(dc, coef + static_cast<int64_t>(s) * E, E, lane, 0.f);
+        const F2 dl = both(dloss[s]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) dc.v[i][h] = mul2(dc.v[i][h], dl);
+      }
     }
     fetch();
     Row<NV> p;
@@ -321,11 +332,11 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
     float g;
     ring.take(p, pick, g, E, lane);
     if (lane >= K) pick = -1;
-    Row<NV> a;
+    Row<NV> a = dc;
     if (!on || (!dgate && s >= S)) {
       // no gradient reaches this token (whatever its logits hold)
       a.fill(0.f);
-      row_store<NV, VEC>(a, dlogits + t * E, E, lane);
+      row_store<NV, KIND>(a, dlogits + t * E, E, lane);
       continue;
     }
     if (dgate) {
@@ -343,24 +354,18 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
       }
       if (pick >= 0 && lane == lead) row[pick] = sum;
       __syncwarp();
-      row_load<NV, VEC>(a, row, E, lane, 0.f);
+      Row<NV> q;
+      row_load<NV, KIND>(q, row, E, lane, 0.f);
       __syncwarp();
       if (pick >= 0) row[pick] = 0.f;
       __syncwarp();
-    } else {
-      a.fill(0.f);
-    }
-    if (s < S) {
-      Row<NV> c;
-      row_load<NV, VEC>(c, coef + static_cast<int64_t>(s) * E, E, lane, 0.f);
-      const F2 dl = both(dloss[s]);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a.v[i][h] = fma2(c.v[i][h], dl, a.v[i][h]);
+        for (int h = 0; h < 2; ++h) a.v[i][h] = add2(a.v[i][h], q.v[i][h]);
     }
     // with e = exp(l - max): p = e / sum e, sum_j p_j a_j = (sum_j e_j a_j) / sum e
-    row_exp<NV, VEC>(p, offset, E, lane);
+    row_exp<NV, KIND>(p, offset, E, lane);
     F2 ea = mul2(p.v[0][0], a.v[0][0]);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -369,16 +374,16 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         if (i + h > 0) ea = fma2(p.v[i][h], a.v[i][h], ea);
     const float2 ea2 = up(ea);
     const float2 sums = up(warp_sum2(pk(row_lane_sum(p), ea2.x + ea2.y)));
-    const float inv = 1.0f / sums.x;
+    const float inv = rcp_approx(sums.x);
     const F2 inv2 = both(inv), dot = both(-sums.y * inv);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         a.v[i][h] = mul2(mul2(p.v[i][h], inv2), add2(a.v[i][h], dot));
-    row_store<NV, VEC>(a, dlogits + t * E, E, lane);
+    row_store<NV, KIND>(a, dlogits + t * E, E, lane);
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  ring.drain();
 }
 
 }  // namespace
@@ -394,11 +399,11 @@ cudaError_t launch_balance_loss(const float* logits, const float* offset, const 
   int* pcnt = reinterpret_cast<int*>(ws + pl.cnt_off);
   int* pn = reinterpret_cast<int*>(ws + pl.n_off);
   if (pl.blocks > 0) {
-    const cudaError_t e = with_row_shape(E, [&](auto nv, auto vec) {
+    const cudaError_t e = with_row_shape(E, [&](auto nv, auto kind) {
       constexpr int NV = decltype(nv)::value;
-      constexpr bool VEC = decltype(vec)::value != 0;
-      constexpr auto kern = balance_partial_kernel<NV, VEC>;
-      constexpr int ring = BAL_WARPS * RowRing<NV, VEC>::BYTES;
+      constexpr int KIND = decltype(kind)::value;
+      constexpr auto kern = balance_partial_kernel<NV, KIND>;
+      constexpr int ring = BAL_WARPS * RowRing<NV, KIND>::BYTES;
       const size_t smem = ring + static_cast<size_t>(BAL_WARPS + 1) * E * sizeof(float);
       const cudaError_t el = smem_limit<kern>(ring + (BAL_WARPS + 1) * NV * 512);
       if (el != cudaSuccess) return el;
@@ -428,13 +433,13 @@ static cudaError_t route_backward_typed(const float* logits, const float* offset
                                         const float* dgate, const uint8_t* mask, const int* seq,
                                         const float* coef, const float* dloss, int64_t T, int S,
                                         int E, int K, OUT* dlogits, cudaStream_t stream) {
-  return with_row_shape(E, [&](auto nv, auto vec) {
+  return with_row_shape(E, [&](auto nv, auto kind) {
     constexpr int NV = decltype(nv)::value;
-    constexpr bool VEC = decltype(vec)::value != 0;
-    constexpr auto kern = route_backward_kernel<NV, VEC, OUT>;
+    constexpr int KIND = decltype(kind)::value;
+    constexpr auto kern = route_backward_kernel<NV, KIND, OUT>;
     // (the same shared memory for every E of the shape, so that the occupancy
     // looked up once holds for all of them)
-    constexpr int smem = BAL_WARPS * (RowRing<NV, VEC>::BYTES + NV * 512);
+    constexpr int smem = BAL_WARPS * (RowRing<NV, KIND>::BYTES + NV * 512);
     const cudaError_t el = smem_limit<kern>(smem);
     if (el != cudaSuccess) return el;
     // one wave of resident blocks, each an equal range of whole warp steps

@@ -7,15 +7,23 @@
 // by element with the same ownership.
 #pragma once
 
-#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <utility>
 
 #include "packed.cuh"
 #include "ptx.cuh"
 
 namespace moezc {
+
+// How rows of E elements lie in NV vectors of four per lane.
+enum RowKind : int {
+  ROW_ODD = 0,     // E % 4 != 0: element by element
+  ROW_VEC = 1,     // vectors, the last ones past E
+  ROW_WHOLE = 2,   // E == 128 NV: vectors, none to test (a third of the 16384 x 768
+                   // case's instructions were tests and fills)
+};
 
 template <int NV>
 struct Row {
@@ -27,62 +35,46 @@ struct Row {
 };
 
 // Elements past E read as `fill`.
-template <int NV, bool VEC>
-__device__ __forceinline__ void row_load(Row<NV>& r, const float* src, int E,
-                                         int lane, float fill) {
+template <int NV, int KIND>
+__device__ __forceinline__ void row_load(Row<NV>& r, const float* src, int E, int lane,
+                                         float fill) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = 4 * lane + 128 * i;
-    if (VEC) {
-      float4 q = make_float4(fill, fill, fill, fill);
-      if (j < E) q = *reinterpret_cast<const float4*>(src + j);
-      r.v[i][0] = pk(q.x, q.y);
-      r.v[i][1] = pk(q.z, q.w);
-    } else {
+    if (KIND == ROW_ODD) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         r.v[i][h] = pk(j + 2 * h < E ? src[j + 2 * h] : fill,
                        j + 2 * h + 1 < E ? src[j + 2 * h + 1] : fill);
+    } else {
+      float4 q = make_float4(fill, fill, fill, fill);
+      if (KIND == ROW_WHOLE || j < E) q = *reinterpret_cast<const float4*>(src + j);
+      r.v[i][0] = pk(q.x, q.y);
+      r.v[i][1] = pk(q.z, q.w);
     }
   }
 }
 
-template <int NV, bool VEC>
-__device__ __forceinline__ void row_store(const Row<NV>& r, float* __restrict__ dst, int E,
-                                          int lane) {
+template <int NV, int KIND, typename OUT>
+__device__ __forceinline__ void row_store(const Row<NV>& r, OUT* dst, int E, int lane) {
+  constexpr bool BF = sizeof(OUT) == 2;   // rounded once to bf16 (nearest, ties to even)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = 4 * lane + 128 * i;
     const float2 a = up(r.v[i][0]), b = up(r.v[i][1]);
-    if (VEC) {
-      if (j < E) __stcs(reinterpret_cast<float4*>(dst + j), make_float4(a.x, a.y, b.x, b.y));
-    } else {
-      if (j < E) dst[j] = a.x;
-      if (j + 1 < E) dst[j + 1] = a.y;
-      if (j + 2 < E) dst[j + 2] = b.x;
-      if (j + 3 < E) dst[j + 3] = b.y;
-    }
-  }
-}
-
-// Rounded once to bf16 (nearest, ties to even).
-template <int NV, bool VEC>
-__device__ __forceinline__ void row_store(const Row<NV>& r, __nv_bfloat16* __restrict__ dst,
-                                          int E, int lane) {
+    if constexpr (KIND == ROW_ODD) {
+      const float f[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = 4 * lane + 128 * i;
-    const __nv_bfloat162 a = __float22bfloat162_rn(up(r.v[i][0]));
-    const __nv_bfloat162 b = __float22bfloat162_rn(up(r.v[i][1]));
-    if (VEC) {
-      if (j < E)
-        __stcs(reinterpret_cast<uint2*>(dst + j), make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                                            *reinterpret_cast<const uint32_t*>(&b)));
+      for (int c = 0; c < 4; ++c)
+        if (j + c < E) dst[j + c] = static_cast<OUT>(f[c]);
+    } else if constexpr (BF) {
+      const __nv_bfloat162 x = __float22bfloat162_rn(a), y = __float22bfloat162_rn(b);
+      if (KIND == ROW_WHOLE || j < E)
+        __stcs(reinterpret_cast<uint2*>(dst + j), make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                                            *reinterpret_cast<const uint32_t*>(&y)));
     } else {
-      if (j < E) dst[j] = a.x;
-      if (j + 1 < E) dst[j + 1] = a.y;
-      if (j + 2 < E) dst[j + 2] = b.x;
-      if (j + 3 < E) dst[j + 3] = b.y;
+      if (KIND == ROW_WHOLE || j < E)
+        __stcs(reinterpret_cast<float4*>(dst + j), make_float4(a.x, a.y, b.x, b.y));
     }
   }
 }
@@ -112,33 +104,44 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // The row's exponentials exp(l + offset - max), in place; offset may be
 // nullptr.  Absent elements, loaded as -inf, and logits of -inf become 0; a row
 // of nothing but -inf, or with a NaN or +inf, becomes NaN.  (2 to the power of
-// (l - max) log2 e: 2^-22 and |l - max| 2^-24 relative, far inside the error of
-// the sums taken of them.)
-template <int NV, bool VEC>
+// l log2 e - max log2 e in one fma: 2^-22 and |l - max| 2^-24 relative, far
+// inside the error of the sums taken of them, and what rounding max log2 e adds
+// is common to the row and divided out.)
+template <int NV, int KIND>
 __device__ __forceinline__ void row_exp(Row<NV>& r, const float* __restrict__ offset, int E,
                                         int lane) {
   if (offset) {
     Row<NV> o;
-    row_load<NV, VEC>(o, offset, E, lane, 0.f);
+    row_load<NV, KIND>(o, offset, E, lane, 0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) r.v[i][h] = add2(r.v[i][h], o.v[i][h]);
   }
-  float mx = -INFINITY;
+  float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float2 a = up(r.v[i][h]);
-      mx = fmaxf(mx, fmaxf(a.x, a.y));
+      m = fmaxf(m, fmaxf(a.x, a.y));
     }
-  const F2 neg = both(-warp_max(mx)), log2e = both(1.4426950408889634f);
+  m = warp_max(m);
+  if (!(fabsf(m) < 1e37f)) {   // (its product with log2 e might overflow: subtract first)
+    const F2 neg = both(-m);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) r.v[i][h] = add2(r.v[i][h], neg);
+    m = 0.f;
+  }
+  constexpr float LOG2E = 1.4426950408889634f;
+  const F2 neg = both(-m * LOG2E), log2e = both(LOG2E);
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float2 x = up(mul2(add2(r.v[i][h], neg), log2e));
+      const float2 x = up(fma2(r.v[i][h], log2e, neg));
       r.v[i][h] = pk(ex2_approx(x.x), ex2_approx(x.y));
     }
 }
@@ -159,90 +162,127 @@ __device__ __forceinline__ float row_lane_sum(const Row<NV>& r) {
 // copies is all the ordering there is, and DEPTH - 1 tokens are in flight
 // without holding registers (a single row ahead in registers left each token
 // waiting for most of a memory latency).
-template <int NV, bool VEC>
+template <int NV, int KIND>
 struct RowRing {
   static constexpr int WORDS = NV * 128 + 64;       // of a stage
   static constexpr int DEPTH = NV >= 8 ? 2 : NV >= 6 ? 3 : NV >= 4 ? 4 : NV >= 3 ? 5 : 6;
   static constexpr int BYTES = DEPTH * WORDS * 4;   // per warp
-  float* base;
-  int put = 0, got = 0;   // stages of the next fetch and the next wait
+  uint32_t base;          // the warp's stages, plus this lane's 16 bytes of a vector
+  uint32_t put, got;      // byte offsets of the next fetch and the next wait
 
-  static __device__ __forceinline__ void copy4(float* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
-                 : "memory");
-  }
+  __device__ __forceinline__ RowRing(float* smem, int lane)
+      : base(smem_u32(smem) + 16 * lane), put(0), got(0) {}
+
   // The row at src and, per lane < K, words of a and b (nullptr: none).  One
   // call a token (or `none`), in order.
   __device__ __forceinline__ void fetch(const float* src, const int* a, const float* b, int E,
                                         int K, int lane) {
-    float* st = base + put * WORDS;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int j = 4 * lane + 128 * i;
-      if (VEC) {
-        if (j < E)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(st + j)),
-                       "l"(src + j)
-                       : "memory");
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (j + c < E) copy4(st + j + c, src + j + c);
-      }
-    }
+    const uint32_t st = base + put;
+    copy(st, src + 4 * lane, E - 4 * lane, std::make_integer_sequence<int, NV>());
     if (lane < K) {
-      if (a) copy4(st + NV * 128 + lane, a + lane);
-      if (b) copy4(st + NV * 128 + 32 + lane, b + lane);
+      const uint32_t w = st - 12 * lane;   // (4 bytes a lane)
+      if (a)
+        asm volatile("cp.async.ca.shared.global [%0+%2], [%1], 4;" ::"r"(w), "l"(a + lane),
+                     "n"(512 * NV)
+                     : "memory");
+      if (b)
+        asm volatile("cp.async.ca.shared.global [%0+%2], [%1], 4;" ::"r"(w), "l"(b + lane),
+                     "n"(512 * NV + 128)
+                     : "memory");
     }
     none();
   }
   __device__ __forceinline__ void none() {
     asm volatile("cp.async.commit_group;" ::: "memory");
-    put = put + 1 == DEPTH ? 0 : put + 1;
+    put = put == (DEPTH - 1) * WORDS * 4 ? 0 : put + WORDS * 4;
   }
   // Waits for the oldest token fetched, DEPTH - 1 others staying in flight, and
   // takes it: its row, and this lane's words.
   __device__ __forceinline__ void take(Row<NV>& r, int& a, float& b, int E, int lane) {
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-    const float* st = base + got * WORDS;
-    row_load<NV, true>(r, st, VEC ? E : NV * 128, lane, -INFINITY);
-    if (!VEC) row_cut(r, E, lane);
-    a = reinterpret_cast<const int*>(st)[NV * 128 + lane];
-    b = st[NV * 128 + 32 + lane];
-    got = got + 1 == DEPTH ? 0 : got + 1;
+    const uint32_t st = base + got;
+    read(r, st, E - 4 * lane, std::make_integer_sequence<int, NV>());
+    const uint32_t w = st - 12 * lane;
+    asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(a) : "r"(w), "n"(512 * NV) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1+%2];" : "=f"(b) : "r"(w), "n"(512 * NV + 128) : "memory");
+    got = got == (DEPTH - 1) * WORDS * 4 ? 0 : got + WORDS * 4;
   }
-  // -inf past E, where a vector of four may cross it
-  static __device__ __forceinline__ void row_cut(Row<NV>& r, int E, int lane) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 4 * lane + 128 * i + 2 * h;
-        const float2 a = up(r.v[i][h]);
-        r.v[i][h] = pk(j < E ? a.x : -INFINITY, j + 1 < E ? a.y : -INFINITY);
-      }
+
+ private:
+  // (vector by vector with the offsets as constants; left: elements of the row
+  // from this lane's first one on)
+  template <int... I>
+  static __device__ __forceinline__ void copy(uint32_t st, const float* s, int left,
+                                              std::integer_sequence<int, I...>) {
+    (copy1<I>(st, s, left), ...);
   }
+  template <int I>
+  static __device__ __forceinline__ void copy1(uint32_t st, const float* s, int left) {
+    if constexpr (KIND == ROW_ODD) {
+      copy_word<512 * I>(st, s, left - 128 * I);
+      copy_word<512 * I + 4>(st, s, left - 128 * I - 1);
+      copy_word<512 * I + 8>(st, s, left - 128 * I - 2);
+      copy_word<512 * I + 12>(st, s, left - 128 * I - 3);
+    } else if (KIND == ROW_WHOLE || left > 128 * I) {
+      asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%2], 16;" ::"r"(st), "l"(s),
+                   "n"(512 * I)
+                   : "memory");
+    }
+  }
+  template <int OFF>
+  static __device__ __forceinline__ void copy_word(uint32_t st, const float* s, int left) {
+    if (left > 0)
+      asm volatile("cp.async.ca.shared.global [%0+%2], [%1+%2], 4;" ::"r"(st), "l"(s), "n"(OFF)
+                   : "memory");
+  }
+  template <int... I>
+  static __device__ __forceinline__ void read(Row<NV>& r, uint32_t st, int left,
+                                              std::integer_sequence<int, I...>) {
+    (read1<I>(r, st, left), ...);
+  }
+  template <int I>
+  static __device__ __forceinline__ void read1(Row<NV>& r, uint32_t st, int left) {
+    float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    if (KIND == ROW_WHOLE || left > 128 * I)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4+%5];"
+                   : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                   : "r"(st), "n"(512 * I)
+                   : "memory");
+    if (KIND == ROW_ODD) {   // a vector may cross the row's end
+      if (left <= 128 * I + 1) q.y = -INFINITY;
+      if (left <= 128 * I + 2) q.z = -INFINITY;
+      if (left <= 128 * I + 3) q.w = -INFINITY;
+    }
+    r.v[I][0] = pk(q.x, q.y);
+    r.v[I][1] = pk(q.z, q.w);
+  }
+
+ public:
+  // Before the block ends: nothing may still be on its way.
+  __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 };
 
-// Calls f with integral constants (vectors per lane, whether rows are read as
-// 16-byte vectors) for rows of E elements.
+// Calls f with integral constants (vectors per lane, kind) for rows of E
+// elements.
 template <int V>
 struct IntC {
   static constexpr int value = V;
 };
 template <typename F>
 inline auto with_row_shape(int E, F&& f) {
-  const bool vec = E % 4 == 0;
-#define MOEZC_ROW(NV)                          \
-  if (E <= 128 * (NV))                         \
-    return vec ? f(IntC<NV>{}, IntC<1>{}) : f(IntC<NV>{}, IntC<0>{});
+#define MOEZC_ROW(NV)                                          \
+  if (E <= 128 * (NV)) {                                       \
+    if (E == 128 * (NV)) return f(IntC<NV>{}, IntC<ROW_WHOLE>{}); \
+    return E % 4 ? f(IntC<NV>{}, IntC<ROW_ODD>{}) : f(IntC<NV>{}, IntC<ROW_VEC>{}); \
+  }
   MOEZC_ROW(1)
   MOEZC_ROW(2)
   MOEZC_ROW(3)
   MOEZC_ROW(4)
   MOEZC_ROW(6)
 #undef MOEZC_ROW
-  return vec ? f(IntC<8>{}, IntC<1>{}) : f(IntC<8>{}, IntC<0>{});
+  if (E == 1024) return f(IntC<8>{}, IntC<ROW_WHOLE>{});
+  return E % 4 ? f(IntC<8>{}, IntC<ROW_ODD>{}) : f(IntC<8>{}, IntC<ROW_VEC>{});
 }
 
 }  // namespace moezc
