@@ -482,8 +482,8 @@ int moe_zc_combine_backward(const void* dout, const void* x, const void* y_rows,
  *                      codes uint8 [n] times one fp32 scale per
  *                      MOE_ZC_ADAMW_BLOCK elements of the tensor
  *                      (exp_avg_scale, exp_avg_sq_scale, fp32 [ceil(n / block)]):
- *                      scale = max(amax, 2^-100) / 448, codes of value * (448 /
- *                      max(amax, 2^-100)) to nearest, ties to even; a positive
+ *                      scale = a (1 / 448) with a = max(amax, 2^-100), codes of
+ *                      value (448 (1 / a)) to nearest, ties to even; a positive
  *                      root never takes the code 0 (it would leave its m divided
  *                      by eps alone).  A block holding a NaN, an infinity or
  *                      2^126 and more gets scale 1.  The step itself uses m and v before rounding.

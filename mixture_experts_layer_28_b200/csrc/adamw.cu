@@ -48,6 +48,7 @@ struct AdamArgs {
   int nt;
   int advance;              // 1: this launch moves the step count on
   AdamHyper h;
+  float one;
   int* step;                // [0] steps done, [1] blocks that have read it (zero between steps)
   const float* lr_scale;    // or nullptr
   const float* grad_scale;  // or nullptr
@@ -219,11 +220,13 @@ __device__ __forceinline__ F2 sqrt2(F2 v) {
   return fma2(e, mul2(y, pk(0.5f, 0.5f)), s);
 }
 
-// Scale of a block from its largest magnitude (bits of a non-negative float,
-// or of an infinity or NaN), and the factor to units of it, 448 / amax through
-// one Newton step of the reciprocal.  A block holding an infinity, a NaN or
-// 2^126 and more gets scale 1 (a NaN keeps the NaN code, what is too large
-// saturates); the floor keeps 448 / amax finite.
+// Scale of a block, amax times the rounded 1 / 448, from its largest magnitude
+// (bits of a non-negative float, or of an infinity or NaN), and the factor to
+// units of it, 448 times the rounded 1 / amax (one Newton step of the
+// reciprocal, whose residual is exact in an fma, leaves it as good as always
+// correctly rounded).  A block holding an infinity, a NaN or 2^126 and more gets
+// scale 1 (a NaN keeps the NaN code, what is too large saturates); the floor
+// keeps 448 / amax finite.
 __device__ __forceinline__ float block_scale(uint32_t amax_bits, float& inv) {
   const bool fine = amax_bits < 0x7E800000u;
   const float a = fmaxf(__uint_as_float(fine ? amax_bits : 0u), 0x1p-100f);
@@ -233,20 +236,23 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits, float& inv) {
 }
 
 struct Coef {
-  F2 b1, omb1, b2, omb2, eps, decay, neg_step, rs, gscale;
+  F2 b1, omb1, b2, omb2, eps, decay, neg_step, rs, gscale, one;
 };
 
 // m, v and p of eight elements; r = sqrt(v).  m and v are rounded product by
-// product (no contraction): they decide codes, which a reference in plain
-// fp32 operations then shares.  The step's quotient is an approximation to an
-// ulp or two: the weight moves by a small part of itself.
+// product: they decide codes, which a reference in plain fp32 operations then
+// shares bit for bit (a value that falls on the other side of a code's border
+// is 6% off).  The sum is an fma with a 1 that the compiler does not know: it
+// contracts a packed product and sum into one rounding, explicit rounding or not.
+// The step's quotient is an approximation to an ulp or two: the weight moves by
+// a small part of itself.
 __device__ __forceinline__ void adam8(F2 (&p)[4], const F2 (&g)[4], F2 (&m)[4], F2 (&v)[4],
                                       F2 (&r)[4], const Coef& c) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const F2 gi = mul2(g[i], c.gscale);
-    m[i] = add2(mul2(m[i], c.b1), mul2(gi, c.omb1));
-    v[i] = add2(mul2(v[i], c.b2), mul2(mul2(gi, gi), c.omb2));
+    m[i] = fma2(mul2(m[i], c.b1), c.one, mul2(gi, c.omb1));
+    v[i] = fma2(mul2(v[i], c.b2), c.one, mul2(mul2(gi, gi), c.omb2));
     r[i] = sqrt2(v[i]);
     const float2 den = up(fma2(r[i], c.rs, c.eps));
     const F2 q = mul2(m[i], pk(rcp_approx(den.x), rcp_approx(den.y)));
@@ -266,10 +272,12 @@ struct Types {
   static constexpr int THREADS = 128;
   static constexpr int WARPS = THREADS / 32;
   // a warp's groups in flight (8 bits: 12 bytes a lane and element fewer, so two;
-  // measured 0.701 against 0.784 ms with one at 403M elements, bf16; fp32 states:
+  // measured 0.71 against 0.81 ms with one at 403M elements, bf16; fp32 states:
   // 206 against 220 us with one at 60M)
   static constexpr int GROUPS = BITS8 ? 2 : 1;
-  static constexpr int BLOCKS = 7;    // resident blocks per SM (72 registers)
+  // resident blocks per SM (8 bits: 708 us with 7, 734 with 6, 736 with 8; fp32
+  // states, 40M elements: 178 with 6, 185 with 7)
+  static constexpr int BLOCKS = BITS8 && !MASTER ? 7 : 6;
   static constexpr int UE = WARPS * GROUPS * ADAM_BLOCK;   // elements of a unit
 };
 
@@ -393,6 +401,7 @@ adamw_kernel(const __grid_constant__ AdamArgs<MAXT> a) {
     c.neg_step = both(static_cast<float>(-lr / one_minus_pow(a.h.beta1, n)));
     c.rs = both(static_cast<float>(rsqrt(one_minus_pow(a.h.beta2, n))));
     c.gscale = both(a.grad_scale ? *a.grad_scale : 1.0f);
+    c.one = both(a.one);
     coef_s = c;
     if (a.advance) {
       __threadfence();   // the step count is read before this block counts itself
@@ -442,6 +451,7 @@ cudaError_t launch_some(const AdamTensor* t, int nt, bool advance, const AdamHyp
   a.nt = nt;
   a.advance = advance ? 1 : 0;
   a.h = h;
+  a.one = 1.0f;
   a.step = step;
   a.lr_scale = lr_scale;
   a.grad_scale = grad_scale;

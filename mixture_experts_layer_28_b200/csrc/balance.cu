@@ -39,13 +39,13 @@ template <int NV, int KIND>
 __device__ __forceinline__ void row_put(const Row<NV>& r, float* dst, int E, int lane) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int j = 4 * lane + 128 * i;
+    const int j = row_elem<KIND>(lane, i, 0);
     const float2 a = up(r.v[i][0]), b = up(r.v[i][1]);
     if (KIND == ROW_ODD) {
       const float f[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (j + c < E) dst[j + c] = f[c];
+        if (j + 32 * c < E) dst[j + 32 * c] = f[c];
     } else if (KIND == ROW_WHOLE || j < E) {
       *reinterpret_cast<float4*>(dst + j) = make_float4(a.x, a.y, b.x, b.y);
     }
@@ -84,7 +84,7 @@ __device__ __forceinline__ unsigned on_bits(const uint8_t* __restrict__ mask, in
 // so no two pairs share a slot and blocks + sequences slots are enough.  Warp w
 // takes tokens w, w + BAL_WARPS, ... of the block's range.
 template <int NV, int KIND>
-__global__ void __launch_bounds__(BAL_THREADS, 2)
+__global__ void __launch_bounds__(BAL_THREADS, bal_blocks(NV))
 balance_partial_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                        const int* __restrict__ idx, const uint8_t* __restrict__ mask,
                        const int* __restrict__ seq, int64_t T, int S, int E, int K, int chunk,
@@ -265,7 +265,7 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
 // only at a boundary.  The picks' dgate are added into a row of shared memory
 // per warp (zero between tokens).
 template <int NV, int KIND, typename OUT>
-__global__ void __launch_bounds__(BAL_THREADS, 2)
+__global__ void __launch_bounds__(BAL_THREADS, bal_blocks(NV))
 route_backward_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                       const int* __restrict__ idx, const float* __restrict__ dgate,
                       const uint8_t* __restrict__ mask, const int* __restrict__ seq,

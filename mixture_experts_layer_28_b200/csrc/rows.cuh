@@ -1,10 +1,11 @@
 // rows.cuh -- one warp's access to a row of E fp32 logits, shared by the
 // kernels with which the router learns (balance.cu).
 //
-// Lane l owns elements 4 l + 128 i + c (i < NV, c < 4), held as pairs: with
-// E % 4 == 0 (all rows then start on 16 bytes) a row is read and written as
-// 16-byte vectors, 512 contiguous bytes per warp instruction; otherwise element
-// by element with the same ownership.
+// With E % 4 == 0 (all rows then start on 16 bytes) lane l owns elements
+// 4 l + 128 i + c (i < NV, c < 4) and a row is read and written as 16-byte
+// vectors, 512 contiguous bytes per warp instruction; otherwise elements
+// l + 128 i + 32 c, one by one, 128 contiguous bytes at a time.  A lane's
+// elements are held as pairs.
 #pragma once
 
 #include <cmath>
@@ -25,6 +26,12 @@ enum RowKind : int {
                    // case's instructions were tests and fills)
 };
 
+// Element c of vector i of a lane.
+template <int KIND>
+__device__ __forceinline__ int row_elem(int lane, int i, int c) {
+  return KIND == ROW_ODD ? lane + 128 * i + 32 * c : 4 * lane + 128 * i + c;
+}
+
 template <int NV>
 struct Row {
   F2 v[NV][2];
@@ -40,12 +47,13 @@ __device__ __forceinline__ void row_load(Row<NV>& r, const float* src, int E, in
                                          float fill) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int j = 4 * lane + 128 * i;
+    const int j = row_elem<KIND>(lane, i, 0);
     if (KIND == ROW_ODD) {
+      float f[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        r.v[i][h] = pk(j + 2 * h < E ? src[j + 2 * h] : fill,
-                       j + 2 * h + 1 < E ? src[j + 2 * h + 1] : fill);
+      for (int c = 0; c < 4; ++c) f[c] = j + 32 * c < E ? src[j + 32 * c] : fill;
+      r.v[i][0] = pk(f[0], f[1]);
+      r.v[i][1] = pk(f[2], f[3]);
     } else {
       float4 q = make_float4(fill, fill, fill, fill);
       if (KIND == ROW_WHOLE || j < E) q = *reinterpret_cast<const float4*>(src + j);
@@ -60,13 +68,13 @@ __device__ __forceinline__ void row_store(const Row<NV>& r, OUT* dst, int E, int
   constexpr bool BF = sizeof(OUT) == 2;   // rounded once to bf16 (nearest, ties to even)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int j = 4 * lane + 128 * i;
+    const int j = row_elem<KIND>(lane, i, 0);
     const float2 a = up(r.v[i][0]), b = up(r.v[i][1]);
     if constexpr (KIND == ROW_ODD) {
       const float f[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (j + c < E) dst[j + c] = static_cast<OUT>(f[c]);
+        if (j + 32 * c < E) dst[j + 32 * c] = static_cast<OUT>(f[c]);
     } else if constexpr (BF) {
       const __nv_bfloat162 x = __float22bfloat162_rn(a), y = __float22bfloat162_rn(b);
       if (KIND == ROW_WHOLE || j < E)
@@ -165,22 +173,24 @@ __device__ __forceinline__ float row_lane_sum(const Row<NV>& r) {
 template <int NV, int KIND>
 struct RowRing {
   static constexpr int WORDS = NV * 128 + 64;       // of a stage
-  static constexpr int DEPTH = NV >= 8 ? 2 : NV >= 6 ? 3 : NV >= 4 ? 4 : NV >= 3 ? 5 : 6;
+  static constexpr int DEPTH = NV >= 8 ? 2 : NV >= 6 ? 3 : NV >= 3 ? 4 : 6;
   static constexpr int BYTES = DEPTH * WORDS * 4;   // per warp
-  uint32_t base;          // the warp's stages, plus this lane's 16 bytes of a vector
+  static constexpr int MINE = KIND == ROW_ODD ? 4 : 16;   // a lane's bytes of an access
+  uint32_t base;          // the warp's stages, plus this lane's part of an access
   uint32_t put, got;      // byte offsets of the next fetch and the next wait
 
   __device__ __forceinline__ RowRing(float* smem, int lane)
-      : base(smem_u32(smem) + 16 * lane), put(0), got(0) {}
+      : base(smem_u32(smem) + MINE * lane), put(0), got(0) {}
 
   // The row at src and, per lane < K, words of a and b (nullptr: none).  One
   // call a token (or `none`), in order.
   __device__ __forceinline__ void fetch(const float* src, const int* a, const float* b, int E,
                                         int K, int lane) {
     const uint32_t st = base + put;
-    copy(st, src + 4 * lane, E - 4 * lane, std::make_integer_sequence<int, NV>());
+    const int first = row_elem<KIND>(lane, 0, 0);
+    copy(st, src + first, E - first, std::make_integer_sequence<int, NV>());
     if (lane < K) {
-      const uint32_t w = st - 12 * lane;   // (4 bytes a lane)
+      const uint32_t w = st - (MINE - 4) * lane;   // (4 bytes a lane)
       if (a)
         asm volatile("cp.async.ca.shared.global [%0+%2], [%1], 4;" ::"r"(w), "l"(a + lane),
                      "n"(512 * NV)
@@ -201,8 +211,8 @@ struct RowRing {
   __device__ __forceinline__ void take(Row<NV>& r, int& a, float& b, int E, int lane) {
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
     const uint32_t st = base + got;
-    read(r, st, E - 4 * lane, std::make_integer_sequence<int, NV>());
-    const uint32_t w = st - 12 * lane;
+    read(r, st, E - row_elem<KIND>(lane, 0, 0), std::make_integer_sequence<int, NV>());
+    const uint32_t w = st - (MINE - 4) * lane;
     asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(a) : "r"(w), "n"(512 * NV) : "memory");
     asm volatile("ld.shared.f32 %0, [%1+%2];" : "=f"(b) : "r"(w), "n"(512 * NV + 128) : "memory");
     got = got == (DEPTH - 1) * WORDS * 4 ? 0 : got + WORDS * 4;
@@ -220,9 +230,9 @@ struct RowRing {
   static __device__ __forceinline__ void copy1(uint32_t st, const float* s, int left) {
     if constexpr (KIND == ROW_ODD) {
       copy_word<512 * I>(st, s, left - 128 * I);
-      copy_word<512 * I + 4>(st, s, left - 128 * I - 1);
-      copy_word<512 * I + 8>(st, s, left - 128 * I - 2);
-      copy_word<512 * I + 12>(st, s, left - 128 * I - 3);
+      copy_word<512 * I + 128>(st, s, left - 128 * I - 32);
+      copy_word<512 * I + 256>(st, s, left - 128 * I - 64);
+      copy_word<512 * I + 384>(st, s, left - 128 * I - 96);
     } else if (KIND == ROW_WHOLE || left > 128 * I) {
       asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%2], 16;" ::"r"(st), "l"(s),
                    "n"(512 * I)
@@ -243,18 +253,23 @@ struct RowRing {
   template <int I>
   static __device__ __forceinline__ void read1(Row<NV>& r, uint32_t st, int left) {
     float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (KIND == ROW_WHOLE || left > 128 * I)
+    if constexpr (KIND == ROW_ODD) {
+      read_word<512 * I>(q.x, st, left - 128 * I);
+      read_word<512 * I + 128>(q.y, st, left - 128 * I - 32);
+      read_word<512 * I + 256>(q.z, st, left - 128 * I - 64);
+      read_word<512 * I + 384>(q.w, st, left - 128 * I - 96);
+    } else if (KIND == ROW_WHOLE || left > 128 * I) {
       asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4+%5];"
                    : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
                    : "r"(st), "n"(512 * I)
                    : "memory");
-    if (KIND == ROW_ODD) {   // a vector may cross the row's end
-      if (left <= 128 * I + 1) q.y = -INFINITY;
-      if (left <= 128 * I + 2) q.z = -INFINITY;
-      if (left <= 128 * I + 3) q.w = -INFINITY;
     }
     r.v[I][0] = pk(q.x, q.y);
     r.v[I][1] = pk(q.z, q.w);
+  }
+  template <int OFF>
+  static __device__ __forceinline__ void read_word(float& x, uint32_t st, int left) {
+    if (left > 0) asm volatile("ld.shared.f32 %0, [%1+%2];" : "=f"(x) : "r"(st), "n"(OFF) : "memory");
   }
 
  public:

@@ -8,6 +8,7 @@ the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -366,9 +367,9 @@ def _on(stream):
 def _empty(stream, dev, *specs):
     """Uninitialised tensors of the given (shape, dtype) on the call's stream."""
     if stream is None:
-        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
+        return [torch.empty(*shape, dtype=dtype, device=dev) for shape, dtype in specs]
     with _on(stream):
-        return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in specs]
+        return [torch.empty(*shape, dtype=dtype, device=dev) for shape, dtype in specs]
 
 
 def _arg(t: Optional[torch.Tensor], dtype, shape, name: str, dev: int) -> Optional[int]:
@@ -440,6 +441,13 @@ def _row_args(logits, idx, logit_offset, mask, seq_start, dev):
             _arg(seq_start, torch.int32, (S + 1,), "seq_start", dev))
 
 
+@functools.lru_cache(maxsize=256)
+def _balance_workspace(T: int, S: int, E: int) -> int:
+    n = ctypes.c_int64(0)
+    _check(lib().moe_zc_balance_workspace(T, S, E, ctypes.byref(n)), "moe_zc_balance_workspace")
+    return n.value
+
+
 def balance_loss(logits: torch.Tensor, idx: torch.Tensor,
                  logit_offset: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
                  seq_start: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
@@ -454,20 +462,19 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor,
     dev = _current_device()
     T, E, K, S, lp, op, ip, mp, sp = _row_args(logits, idx, logit_offset, mask, seq_start, dev)
     wp = _arg(weight, torch.float32, (E,), "weight", dev)
-    nbytes = ctypes.c_int64(0)
-    L = lib()
-    _check(L.moe_zc_balance_workspace(T, S, E, ctypes.byref(nbytes)), "moe_zc_balance_workspace")
-    f32 = torch.float32
-    # (coef first: it is the one that has to be 16-byte aligned)
-    table, loss, ws = _empty(stream, logits.device, ((3, S, E), f32), ((S,), f32),
-                             ((nbytes.value,), torch.uint8))
-    coef, prob, counts = table.unbind(0)
-    counts = counts.view(torch.int32)
-    _check(L.moe_zc_balance_loss(lp, op, ip, mp, sp, wp, T, S, E, K, loss.data_ptr(),
-                                 counts.data_ptr(), prob.data_ptr(), coef.data_ptr(),
-                                 ws.data_ptr(), nbytes.value, _stream_of(stream, dev)),
+    # One buffer (an allocation costs more than the views of it): coef first, as
+    # it has to be 16-byte aligned, prob, counts, loss, then the workspace.
+    n, nbytes = S * E, _balance_workspace(T, S, E)
+    ws = (3 * n + S + 3) // 4 * 4
+    (buf,) = _empty(stream, logits.device, ((ws + nbytes // 4,), torch.float32))
+    p = buf.data_ptr()
+    _check(lib().moe_zc_balance_loss(lp, op, ip, mp, sp, wp, T, S, E, K, p + 12 * n, p + 8 * n,
+                                     p + 4 * n, p, p + 4 * ws, nbytes, _stream_of(stream, dev)),
            "moe_zc_balance_loss")
-    return BalanceLoss(loss, counts, prob, coef)
+    shape, strides = (S, E), (E, 1)
+    return BalanceLoss(buf.as_strided((S,), (1,), 3 * n),
+                       buf.view(torch.int32).as_strided(shape, strides, 2 * n),
+                       buf.as_strided(shape, strides, n), buf.as_strided(shape, strides, 0))
 
 
 def route_backward(logits: torch.Tensor, idx: Optional[torch.Tensor] = None,

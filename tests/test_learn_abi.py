@@ -35,7 +35,10 @@ def test_workspace_holds_a_slot_for_every_block_and_sequence(L):
     for T in (0, 1, 8, 9, 2368, 2369, 16384, 100000):
         for S in (0, 1, 7, 3000):
             st, n = workspace(L, T, S, 20)
-            chunk = max(8, -(-T // 296))
+            # one wave (three blocks on each of 148 multiprocessors) of at least 8 tokens,
+            # of 16 where there are more than one wave of 8
+            chunk = max(8, -(-T // 444))
+            chunk = 16 if 8 < chunk < 16 else chunk
             slots = -(-T // chunk) + S
             assert st == mz.OK and n >= slots * (20 * 8 + 4)
     assert L.moe_zc_balance_workspace(4, 1, 4, None) == mz.ERR_INVALID_ARG
