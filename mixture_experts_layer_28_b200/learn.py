@@ -1,0 +1,99 @@
+"""One training step of the layer's router, experts frozen.
+
+LongCat-Flash write-up ("Meituan's large model goes viral for its speed"),
+section "Zero-computation experts": the router is learnt with the model, and
+the expert bias follows recent expert usage outside the training loss.  Here
+the router's weight W_r learns from the layer's output gradient and from a
+balance loss on its probabilities, and the bias may follow the same counts:
+
+  forward    moe_zc_route_logits, moe_zc_dispatch, moe_zc_experts,
+             moe_zc_combine: the layer, with the logits kept
+  backward   moe_zc_combine_backward: the gates' gradient from dout
+             moe_zc_balance_loss: the loss of each sequence, its counts and
+             its gradient's coefficients
+             moe_zc_route_backward: both into the logits' gradient (bf16)
+             dW_r = dlogits^T x, a plain matrix product (the library's own is
+             torch's)
+  step       moe_zc_adamw on W_r
+
+all on the current stream.  As in ep.py, one host read-back per forward sizes
+the dispatched rows.  Gradients of several ranks' batches are summed by the
+caller between backward and step.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import moe_zc as mz
+
+
+class RouterGrad(NamedTuple):
+    W_r: torch.Tensor               # bf16 [E, d]
+    balance: mz.BalanceLoss         # loss, counts, prob, coef of the step's sequences
+
+
+class RouterStep:
+    """The router's training step around frozen experts.
+
+    W_r bf16 [E, d] is updated in place by step(); b fp32 [E] (the expert bias)
+    and the experts' weights are used as they are.  balance scales the balance
+    loss (averaged over the sequences); weight (fp32 [E]) holds the inverse
+    target shares of the experts (balance_loss).  The remaining arguments are
+    AdamW's.
+    """
+
+    def __init__(self, N: int, Z: int, K: int, W_r: torch.Tensor, b: torch.Tensor,
+                 W_gate: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor, lr: float,
+                 balance: float = 1e-2, weight: Optional[torch.Tensor] = None,
+                 betas=(0.9, 0.95), eps: float = 1e-8, weight_decay: float = 0.1,
+                 state_bits: int = 32, master=True):
+        if N < 1:
+            raise ValueError("a router of zero experts alone has nothing to dispatch (N < 1)")
+        self.N, self.Z, self.K = N, Z, K
+        self.W_r, self.b = W_r, b
+        self.experts = (W_gate, W_up, W_down)
+        self.balance, self.weight = balance, weight
+        self.opt = mz.AdamW([W_r], lr, betas, eps, weight_decay, state_bits, master=master or None)
+        self._saved = None
+
+    def forward(self, x: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                seq_start: Optional[torch.Tensor] = None,
+                logit_offset: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The layer's output for x bf16 [T, d]; mask and seq_start as for
+        balance_loss.  Keeps what backward needs."""
+        logits, idx, gate, zsum, counts = mz.route_logits(x, self.W_r, self.b, self.N, self.Z,
+                                                          self.K, logit_offset)
+        rows = int(counts[: self.N].sum())          # the one host read-back
+        slot, send, expert = mz.dispatch(x, idx, counts, self.N, rows)
+        y = mz.experts(send, expert, 0, *self.experts)
+        self._saved = (x, logits, idx, gate, slot, y, mask, seq_start, logit_offset)
+        return mz.combine(x, y, slot, gate, zsum)
+
+    def backward(self, dout: torch.Tensor) -> RouterGrad:
+        """Gradient of W_r from the output's gradient dout bf16 [T, d] and the
+        balance loss; consumes what forward kept."""
+        if self._saved is None:
+            raise RuntimeError("backward needs a forward before it")
+        x, logits, idx, gate, slot, y, mask, seq_start, off = self._saved
+        self._saved = None
+        dgate, _ = mz.combine_backward(dout, x, y, slot, gate, rows=False)
+        r = mz.balance_loss(logits, idx, off, mask, seq_start, self.weight)
+        S = r.loss.shape[0]
+        dloss = torch.full((S,), self.balance / max(S, 1), device=x.device)
+        dlogits = mz.route_backward(logits, idx, dgate, r.coef, dloss, off, mask, seq_start,
+                                    dtype=torch.bfloat16)
+        return RouterGrad(dlogits.t() @ x, r)
+
+    def step(self, grad: torch.Tensor, lr_scale: Optional[torch.Tensor] = None,
+             grad_scale: Optional[torch.Tensor] = None) -> None:
+        """AdamW on W_r with its gradient (RouterGrad.W_r, summed over ranks)."""
+        self.opt.step([grad], lr_scale, grad_scale)
+
+    def follow_load(self, controller: mz.BiasController, counts: torch.Tensor,
+                    tokens: int) -> None:
+        """Moves the expert bias by the load counts (int32 [S, E] or [E], as
+        RouterGrad.balance.counts) of `tokens` tokens."""
+        load = counts.sum(0) if counts.dim() == 2 else counts
+        self.b.copy_(torch.from_numpy(controller.step(load.cpu().numpy(), tokens)))
