@@ -28,7 +28,7 @@
 // The tensors' addresses travel in the launch's parameters (no copy to the
 // device, so a captured step replays as it is), and the step count lives on the
 // device: the last block to have read it moves it on.
-#include "kernels.cuh"
+#include "learn.cuh"
 #include "packed.cuh"
 #include "ptx.cuh"
 

@@ -17,7 +17,7 @@
 // the tokens of its own range in a fixed order and leaves partial sums, and a
 // second kernel adds those in block order, so results do not change from run
 // to run.
-#include "kernels.cuh"
+#include "learn.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
 

@@ -16,7 +16,7 @@
 // flight 755; loads marked too 602).  Few tokens (one wave) are cut along the
 // row over a cluster of up to 8 blocks, whose partial dots meet in the first
 // one's shared memory.
-#include "kernels.cuh"
+#include "learn.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
 

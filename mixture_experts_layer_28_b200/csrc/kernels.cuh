@@ -107,27 +107,6 @@ inline cudaError_t launch_pdl_pairs(void (*kernel)(KArgs...), dim3 grid, dim3 bl
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// launch_pdl as clusters of `cluster` CTAs along x (a divisor of the grid).
-template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), unsigned cluster, dim3 grid,
-                                      dim3 block, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
 // Multiprocessors of the current device (cached).
 inline int device_sms() {
   static int cached[64] = {0};
@@ -355,10 +334,9 @@ cudaError_t launch_permute_fp8(const __nv_bfloat16* x, const int* idx, const int
 // softmax over E logits (+offset), + bias, top-K, zero-gate sums, histogram.
 // The logits may come as `splits` partial sums [splits][T][E], added in
 // slice order.
-// lout (optional, with splits > 1): the summed logits [T][E], before the offset.
 cudaError_t launch_route(const float* logits, const float* b, const float* offset, int64_t T,
                          int E, int N, int K, int* idx, float* gate, float* zsum, int* cnt,
-                         cudaStream_t stream, int splits = 1, float* lout = nullptr);
+                         cudaStream_t stream, int splits = 1);
 
 // ------------------------------------------------------------------ dispatch
 // Slot assignment with the experts' row and tile offsets (grp_off, grp_ttp
@@ -386,68 +364,5 @@ cudaError_t launch_permute(const __nv_bfloat16* x, const int* slot, int64_t T, i
 cudaError_t launch_combine(const __nv_bfloat16* x, const __nv_bfloat16* Y, const int* slot,
                            const float* gate, const float* zsum, int64_t T, int d, int K,
                            __nv_bfloat16* out, cudaStream_t stream);
-
-// ------------------------------------------------------------------ learning
-// The balance loss (balance.cu).  Tokens are cut into `blocks` ranges of
-// `chunk`; its workspace holds, for each of blocks + S (range, sequence)
-// slots, E partial sums, E partial counts and the number of counted tokens.
-// One wave of resident blocks on the 148 multiprocessors of a B200 (three per
-// multiprocessor up to 384 experts, else two), each with at least one token per
-// warp.
-struct BalancePlan {
-  int64_t blocks;
-  int chunk;
-  size_t cnt_off, n_off, bytes;
-};
-constexpr int bal_blocks(int nv) { return nv <= 3 ? 3 : 2; }   // nv = ceil(E / 128)
-inline BalancePlan balance_plan(int64_t T, int S, int E) {
-  BalancePlan p;
-  const int grid = bal_blocks((E + 127) / 128) * 148;
-  const int64_t want = (T + grid - 1) / grid;
-  p.chunk = static_cast<int>(want < 8 ? 8 : want);
-  // (a few more tokens a block rather than more partial sums to add: 4096 x 96
-  // 9.3 -> 7.5 us)
-  if (p.chunk > 8 && p.chunk < 16) p.chunk = 16;
-  p.blocks = (T + p.chunk - 1) / p.chunk;
-  const size_t slots = static_cast<size_t>(p.blocks) + S;
-  const size_t part = (slots * E * sizeof(float) + 255) / 256 * 256;
-  p.cnt_off = part;
-  p.n_off = 2 * part;
-  p.bytes = 2 * part + (slots * sizeof(int) + 255) / 256 * 256;
-  return p;
-}
-// seq: [S + 1] offsets or nullptr (S == 1: all T tokens).
-cudaError_t launch_balance_loss(const float* logits, const float* offset, const int* idx,
-                                const uint8_t* mask, const int* seq, const float* weight,
-                                int64_t T, int S, int E, int K, float* loss, int* counts,
-                                float* prob, float* coef, void* workspace, cudaStream_t stream);
-// dgate or coef (with dloss and seq) may be nullptr; dlogits fp32 or bf16.
-cudaError_t launch_route_backward(const float* logits, const float* offset, const int* idx,
-                                  const float* dgate, const uint8_t* mask, const int* seq,
-                                  const float* coef, const float* dloss, int64_t T, int S, int E,
-                                  int K, void* dlogits, bool bf16, cudaStream_t stream);
-// dY may be nullptr; rows: the rows of Y and dY (slots past them are not followed).
-cudaError_t launch_combine_backward(const __nv_bfloat16* dout, const __nv_bfloat16* x,
-                                    const __nv_bfloat16* Y, const int* slot, const float* gate,
-                                    int64_t T, int d, int K, int64_t rows, float* dgate,
-                                    __nv_bfloat16* dY, cudaStream_t stream);
-
-constexpr int ADAM_BLOCK = 256;   // elements per scale of an 8-bit state
-struct AdamTensor {
-  void* p;
-  const void* g;
-  void* m;
-  void* v;
-  float* ms;       // scales of 8-bit states, one per ADAM_BLOCK elements
-  float* vs;
-  float* master;   // fp32 weights (p bf16) or nullptr
-  int64_t n;
-};
-struct AdamHyper {
-  double lr, beta1, beta2, eps, weight_decay;
-};
-cudaError_t launch_adamw(const AdamTensor* t, int nt, bool p_bf16, bool g_bf16, bool master,
-                         bool bits8, const AdamHyper& h, int* step, const float* lr_scale,
-                         const float* grad_scale, cudaStream_t stream);
 
 }  // namespace moezc

@@ -9,7 +9,7 @@
 #include <vector>
 
 #include "../../include/moe_zc.h"
-#include "kernels.cuh"
+#include "learn.cuh"
 
 namespace {
 

@@ -28,7 +28,7 @@
 #include <vector>
 
 #include "../../include/moe_zc.h"
-#include "kernels.cuh"
+#include "learn.cuh"
 
 namespace {
 
@@ -969,8 +969,8 @@ static int route_impl(const void* x, const void* W_r, const float* b, const floa
     const int64_t rg = rp.tiles * rp.splits;
     CK(launch_gemm(MODE_ROUTER, mWr, mWr, mX, mXf, pr, static_cast<int>(rg < c.sms ? rg : c.sms),
                    st));
-    CK(launch_route(glogits, b, logit_offset, T, E, N, K, idx, gate, zsum, counts, st, rp.splits,
-                    direct ? nullptr : logits_out));
+    CK(launch_route_logits(glogits, b, logit_offset, T, E, N, K, idx, gate, zsum, counts, st,
+                           rp.splits, direct ? nullptr : logits_out));
   }
   // (captured into a CUDA graph: no event, as in the forward)
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;

@@ -20,7 +20,7 @@
 // so identity experts never enter dispatch or the FFN GEMMs.  The expert-load
 // histogram counts picks of all E experts, first in shared memory per block,
 // then one global atomic per touched expert per block.
-#include "kernels.cuh"
+#include "learn.cuh"
 #include "ptx.cuh"
 #include "step.cuh"
 
@@ -157,9 +157,9 @@ cudaError_t launch_route_vpl(const float* logits, const float* b, const float* o
 
 }  // namespace
 
-cudaError_t launch_route(const float* logits, const float* b, const float* offset, int64_t T,
-                         int E, int N, int K, int* idx, float* gate, float* zsum, int* cnt,
-                         cudaStream_t stream, int splits, float* lout) {
+cudaError_t launch_route_logits(const float* logits, const float* b, const float* offset,
+                                int64_t T, int E, int N, int K, int* idx, float* gate, float* zsum,
+                                int* cnt, cudaStream_t stream, int splits, float* lout) {
   if (T <= 0) return cudaSuccess;
   if (splits < 1) splits = 1;
 #define MOEZC_ROUTE(V)                                                                     \
@@ -178,6 +178,13 @@ cudaError_t launch_route(const float* logits, const float* b, const float* offse
 #undef MOEZC_ROUTE
   return launch_route_vpl<32>(logits, b, offset, T, E, N, K, idx, gate, zsum, cnt, stream, splits,
                               lout);
+}
+
+cudaError_t launch_route(const float* logits, const float* b, const float* offset, int64_t T,
+                         int E, int N, int K, int* idx, float* gate, float* zsum, int* cnt,
+                         cudaStream_t stream, int splits) {
+  return launch_route_logits(logits, b, offset, T, E, N, K, idx, gate, zsum, cnt, stream, splits,
+                             nullptr);
 }
 
 }  // namespace moezc
