@@ -46,6 +46,7 @@ struct AdamArgs {
   AdamTensor t[MAXT];
   int unit_end[MAXT];       // prefix sum of units, tensor by tensor
   int nt;
+  int iters;                // steps of a unit
   int advance;              // 1: this launch moves the step count on
   AdamHyper h;
   float one;
@@ -75,10 +76,16 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// Maximum that keeps a NaN (as the largest bits).
-__device__ __forceinline__ float max_nan(float a, float b) {
+// Largest magnitude and smallest value of three; the largest keeps a NaN (as the
+// largest bits).
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -275,27 +282,50 @@ struct Types {
   // measured 0.71 against 0.81 ms with one at 403M elements, bf16; fp32 states:
   // 206 against 220 us with one at 60M)
   static constexpr int GROUPS = BITS8 ? 2 : 1;
-  // resident blocks per SM (8 bits: 708 us with 7, 734 with 6, 736 with 8; fp32
-  // states, 40M elements: 178 with 6, 185 with 7)
-  static constexpr int BLOCKS = BITS8 && !MASTER ? 7 : 6;
-  static constexpr int UE = WARPS * GROUPS * ADAM_BLOCK;   // elements of a unit
+  // resident blocks per SM (8 bits, 16 steps a unit: 663 us with 6, 690 with 5;
+  // fp32 states, 40M elements: 178 with 6, 185 with 7)
+  static constexpr int BLOCKS = 6;
+  static constexpr int STEP = WARPS * GROUPS * ADAM_BLOCK;   // elements of a block's step
 };
 
-// A warp's GROUPS groups of a tensor from element e0 (a multiple of ADAM_BLOCK)
-// on.  FULL: all of them lie inside the tensor.
+// Where a warp's next groups of a tensor start in its arrays.
+template <typename Y>
+struct At {
+  typename Y::WT* w;
+  typename Y::PT* p;           // (MASTER) the rounded weight
+  const typename Y::GT* g;
+  typename Y::ST* m;
+  typename Y::ST* v;
+  float* ms;                   // 8 bits
+  float* vs;
+  __device__ __forceinline__ At(const AdamTensor& T, int64_t e0)
+      : w((Y::MASTER ? reinterpret_cast<typename Y::WT*>(T.master)
+                     : static_cast<typename Y::WT*>(T.p)) + e0),
+        p(static_cast<typename Y::PT*>(T.p) + e0),
+        g(static_cast<const typename Y::GT*>(T.g) + e0),
+        m(static_cast<typename Y::ST*>(T.m) + e0),
+        v(static_cast<typename Y::ST*>(T.v) + e0),
+        ms(T.ms + e0 / ADAM_BLOCK),
+        vs(T.vs + e0 / ADAM_BLOCK) {}
+  __device__ __forceinline__ void next() {
+    constexpr int N = Y::GROUPS * ADAM_BLOCK;
+    w += N;
+    if (Y::MASTER) p += N;
+    g += N;
+    m += N;
+    v += N;
+    ms += Y::GROUPS;
+    vs += Y::GROUPS;
+  }
+};
+
+// A warp's next GROUPS groups, of which `left` elements exist (FULL: all).
 template <typename Y, bool FULL>
-__device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int lane,
-                                          const Coef& c) {
+__device__ __forceinline__ void adam_warp(const At<Y>& at, int left, int lane, const Coef& c) {
   using WT = typename Y::WT;
   using ST = typename Y::ST;
   constexpr int NG = Y::GROUPS;
   constexpr bool SP = Y::SPLIT;
-  WT* w = (Y::MASTER ? reinterpret_cast<WT*>(T.master) : static_cast<WT*>(T.p)) + e0;
-  typename Y::PT* pp = static_cast<typename Y::PT*>(T.p) + e0;
-  const typename Y::GT* gp = static_cast<const typename Y::GT*>(T.g) + e0;
-  ST* mp = static_cast<ST*>(T.m) + e0;
-  ST* vp = static_cast<ST*>(T.v) + e0;
-  const int64_t b0 = e0 / ADAM_BLOCK;
   Raw8<WT, SP> rp[NG];
   Raw8<typename Y::GT, SP> rg[NG];
   Raw8<ST, SP> rm[NG], rv[NG];
@@ -304,15 +334,14 @@ __device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int l
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
     const int o = k * ADAM_BLOCK;
-    const int64_t left = FULL ? ADAM_BLOCK : T.n - (e0 + o);
-    n[k] = left >= ADAM_BLOCK ? ADAM_BLOCK : (left > 0 ? static_cast<int>(left) : 0);
-    rp[k].template load<FULL>(w + o, lane, n[k]);
-    rg[k].template load<FULL>(gp + o, lane, n[k]);
-    rm[k].template load<FULL>(mp + o, lane, n[k]);
-    rv[k].template load<FULL>(vp + o, lane, n[k]);
+    n[k] = FULL ? ADAM_BLOCK : max(0, min(ADAM_BLOCK, left - o));
+    rp[k].template load<FULL>(at.w + o, lane, n[k]);
+    rg[k].template load<FULL>(at.g + o, lane, n[k]);
+    rm[k].template load<FULL>(at.m + o, lane, n[k]);
+    rv[k].template load<FULL>(at.v + o, lane, n[k]);
     if (Y::BITS8) {
-      sm[k] = n[k] > 0 ? T.ms[b0 + k] : 0.f;
-      sv[k] = n[k] > 0 ? T.vs[b0 + k] : 0.f;
+      sm[k] = n[k] > 0 ? at.ms[k] : 0.f;
+      sv[k] = n[k] > 0 ? at.vs[k] : 0.f;
     }
   }
 #pragma unroll
@@ -335,11 +364,11 @@ __device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int l
     }
     adam8(p, g, m, v, r, c);
     rp[k].set(p);
-    rp[k].template store<FULL>(w + o, lane, n[k]);
+    rp[k].template store<FULL>(at.w + o, lane, n[k]);
     if (Y::MASTER) {
       Raw8<typename Y::PT, SP> out;
       out.set(p);
-      out.template store<FULL>(pp + o, lane, n[k]);
+      out.template store<FULL>(at.p + o, lane, n[k]);
     }
     if (Y::BITS8) {
       // (elements past the tensor's end are zero: their m and r stay zero)
@@ -347,9 +376,9 @@ __device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int l
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 a = up(m[i]), b = up(r[i]);
-        fm = max_nan(max_nan(fm, fabsf(a.x)), fabsf(a.y));
-        fr = max_nan(max_nan(fr, b.x), b.y);
-        low = fminf(fminf(low, b.x), b.y);
+        fm = max3_abs_nan(fm, a.x, a.y);
+        fr = max3_abs_nan(fr, b.x, b.y);
+        low = min3(low, b.x, b.y);
       }
       float im, ir;
       const float nm = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(fm)), im);
@@ -371,14 +400,14 @@ __device__ __forceinline__ void adam_warp(const AdamTensor& T, int64_t e0, int l
         }
       }
       if (lane == 0) {
-        T.ms[b0 + k] = nm;
-        T.vs[b0 + k] = nr;
+        at.ms[k] = nm;
+        at.vs[k] = nr;
       }
     }
     rm[k].set(m);
     rv[k].set(v);
-    rm[k].template store<FULL>(mp + o, lane, n[k]);
-    rv[k].template store<FULL>(vp + o, lane, n[k]);
+    rm[k].template store<FULL>(at.m + o, lane, n[k]);
+    rv[k].template store<FULL>(at.v + o, lane, n[k]);
   }
 }
 
@@ -425,12 +454,14 @@ adamw_kernel(const __grid_constant__ AdamArgs<MAXT> a) {
     }
     const AdamTensor& T = a.t[ti];
     const int u0 = ti ? a.unit_end[ti - 1] : 0;
-    const int64_t e0 =
-        static_cast<int64_t>(u - u0) * Y::UE + warp * (Y::GROUPS * ADAM_BLOCK);
-    if (e0 + Y::GROUPS * ADAM_BLOCK <= T.n)
-      adam_warp<Y, true>(T, e0, lane, c);
-    else if (e0 < T.n)
-      adam_warp<Y, false>(T, e0, lane, c);
+    constexpr int N = Y::GROUPS * ADAM_BLOCK;
+    const int64_t e0 = (static_cast<int64_t>(u - u0) * Y::WARPS + warp) * (a.iters * N);
+    if (e0 >= T.n) continue;
+    At<Y> at(T, e0);
+    const int64_t all = T.n - e0;
+    int left = all < a.iters * N ? static_cast<int>(all) : a.iters * N;
+    for (; left >= N; left -= N, at.next()) adam_warp<Y, true>(at, N, lane, c);
+    if (left > 0) adam_warp<Y, false>(at, left, lane, c);
   }
   griddep_launch_dependents();
 }
@@ -441,10 +472,20 @@ cudaError_t launch_some(const AdamTensor* t, int nt, bool advance, const AdamHyp
   constexpr auto kern = adamw_kernel<Y, MAXT>;
   const int64_t cap = static_cast<int64_t>(device_sms()) * blocks_per_sm<kern>(Y::THREADS, 0);
   AdamArgs<MAXT> a;
+  // 8 bits: units of up to 16 steps, as long as each resident block gets four
+  // units, so that the look-up of the tensor and the addresses are made once a
+  // unit (403M elements, bf16, under the power cap: 724 us with single steps, 694
+  // with 8, 663 with 16, 672 with 32).  fp32 states wait for memory alone and
+  // keep their blocks side by side: single steps (60M: 206 us, 220 with 8).
+  int64_t steps = 0;
+  for (int i = 0; i < nt; ++i) steps += (t[i].n + Y::STEP - 1) / Y::STEP;
+  a.iters = Y::BITS8 ? 16 : 1;
+  while (a.iters > 1 && steps / a.iters < 4 * cap) a.iters /= 2;
+  const int64_t unit = static_cast<int64_t>(a.iters) * Y::STEP;
   int64_t units = 0;
   for (int i = 0; i < nt; ++i) {
     a.t[i] = t[i];
-    units += (t[i].n + Y::UE - 1) / Y::UE;
+    units += (t[i].n + unit - 1) / unit;
     if (units > 0x7fffffff - cap) return cudaErrorInvalidValue;
     a.unit_end[i] = static_cast<int>(units);
   }
