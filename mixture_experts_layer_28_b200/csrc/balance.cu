@@ -109,6 +109,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
     f += BAL_WARPS;
   };
   for (int i = 0; i < Ring::DEPTH - 1; ++i) fetch();
+  const Offset<NV, KIND> off(offset, E, lane);
   int64_t u = t0 + warp;      // this warp's next token
   unsigned on = 0;            // the mask of its next ones
   int left = 0;               // ... how many bits of it are still ahead
@@ -137,7 +138,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
       float none;
       ring.take(r, pick, none, E, lane);
       if (!counts) continue;
-      row_exp<NV, KIND>(r, offset, E, lane);
+      row_exp<NV, KIND>(r, off, E, lane);
       const F2 inv = both(rcp_approx(warp_sum(row_lane_sum(r))));
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -292,6 +293,7 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
     f += BAL_WARPS;
   };
   for (int i = 0; i < Ring::DEPTH - 1; ++i) fetch();
+  const Offset<NV, KIND> off(offset, E, lane);
   // tokens [sa, se) share s (S: no sequence); none known yet
   int s = S;
   int64_t sa = 0, se = coef ? 0 : T;
@@ -365,7 +367,7 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
         for (int h = 0; h < 2; ++h) a.v[i][h] = add2(a.v[i][h], q.v[i][h]);
     }
     // with e = exp(l - max): p = e / sum e, sum_j p_j a_j = (sum_j e_j a_j) / sum e
-    row_exp<NV, KIND>(p, offset, E, lane);
+    row_exp<NV, KIND>(p, off, E, lane);
     F2 ea = mul2(p.v[0][0], a.v[0][0]);
 #pragma unroll
     for (int i = 0; i < NV; ++i)

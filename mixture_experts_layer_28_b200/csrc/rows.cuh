@@ -109,23 +109,45 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return r;
 }
 
-// The row's exponentials exp(l + offset - max), in place; offset may be
-// nullptr.  Absent elements, loaded as -inf, and logits of -inf become 0; a row
-// of nothing but -inf, or with a NaN or +inf, becomes NaN.  (2 to the power of
-// l log2 e - max log2 e in one fma: 2^-22 and |l - max| 2^-24 relative, far
-// inside the error of the sums taken of them, and what rounding max log2 e adds
-// is common to the row and divided out.)
+// The row of logit offsets (or nothing: nullptr): in registers for short rows,
+// else read again for every token.
 template <int NV, int KIND>
-__device__ __forceinline__ void row_exp(Row<NV>& r, const float* __restrict__ offset, int E,
-                                        int lane) {
-  if (offset) {
-    Row<NV> o;
-    row_load<NV, KIND>(o, offset, E, lane, 0.f);
+struct Offset {
+  static constexpr bool KEPT = NV <= 4;
+  const float* src;
+  Row<KEPT ? NV : 1> row;
+  __device__ __forceinline__ Offset(const float* p, int E, int lane) : src(p) {
+    if constexpr (KEPT) {
+      if (src) row_load<NV, KIND>(row, src, E, lane, 0.f);
+    }
+  }
+  __device__ __forceinline__ void add(Row<NV>& r, int E, int lane) const {
+    if (!src) return;
+    if constexpr (KEPT) {
+      sum(r, row);
+    } else {
+      Row<NV> o;
+      row_load<NV, KIND>(o, src, E, lane, 0.f);
+      sum(r, o);
+    }
+  }
+  static __device__ __forceinline__ void sum(Row<NV>& r, const Row<NV>& o) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) r.v[i][h] = add2(r.v[i][h], o.v[i][h]);
   }
+};
+
+// The row's exponentials exp(l + offset - max), in place.  Absent elements, loaded as -inf, and logits of -inf become 0; a row
+// of nothing but -inf, or with a NaN or +inf, becomes NaN.  (2 to the power of
+// l log2 e - max log2 e in one fma: 2^-22 and |l - max| 2^-24 relative, far
+// inside the error of the sums taken of them, and what rounding max log2 e adds
+// is common to the row and divided out.)
+template <int NV, int KIND>
+__device__ __forceinline__ void row_exp(Row<NV>& r, const Offset<NV, KIND>& offset, int E,
+                                        int lane) {
+  offset.add(r, E, lane);
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
