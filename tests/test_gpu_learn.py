@@ -519,8 +519,10 @@ def test_another_stream():
     raw = run(stream=s.cuda_stream)
     torch.cuda.current_stream().wait_stream(s)
     torch.cuda.synchronize()
-    for a, b, c in zip(want, got, raw):
-        assert torch.equal(a, b) and torch.equal(a, c)
+    default = run(stream=0)
+    torch.cuda.synchronize()
+    for a, b, c, d in zip(want, got, raw, default):
+        assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(a, d)
 
 
 def test_two_captured_graphs_replayed_together():
@@ -568,6 +570,60 @@ def test_adamw_replayed_steps_go_on_counting(bits):
     assert opt.step_count.tolist() == [4, 0] == eager.step_count.tolist()
     for a, b in zip(opt.params, eager.params):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+
+
+def test_rows_past_32_bit_offsets():
+    """2.1 M rows of 1024 logits (8.6 GB): every thousandth row is the same, so the
+    first thousand tell what all the others must be."""
+    n, reps, E, K = 1000, 2100, 1024, 4
+    small, idx = rows_case(n, E, K, seed=21)
+    dgate = torch.randn(n, K, generator=gen(22)).cuda()
+    logits = small.repeat(reps, 1)
+    assert logits.numel() > 2 ** 31
+    big, dbig = idx.repeat(reps, 1), dgate.repeat(reps, 1)
+    want = mz.route_backward(small, idx, dgate=dgate, dtype=torch.bfloat16)
+    got = mz.route_backward(logits, big, dgate=dbig, dtype=torch.bfloat16)
+    assert torch.equal(got.view(reps, n, E)[-1], want) and torch.equal(got.view(reps, n, E)[reps // 2], want)
+    del got
+    seq = ints([0, n * (reps - 1), n * reps])
+    r, one = mz.balance_loss(logits, big, seq_start=seq), mz.balance_loss(small, idx)
+    assert torch.equal(r.counts[1], one.counts[0]) and torch.equal(r.counts[0], one.counts[0] * (reps - 1))
+    # the same tokens' mean, summed in two orders
+    rel = 2 * (ref.softmax_steps(small.cpu()) + 4 * n) * U
+    assert torch.allclose(r.prob[1], one.prob[0], rtol=rel, atol=0)
+
+
+def test_expert_rows_past_32_bit_offsets():
+    """360 000 rows of 6144 features: a token's slots at the far end give what
+    they give near the start."""
+    d, K, R = 6144, 3, 360_000
+    dout, x, y, _, gate = combine_case(4, d, K, 0.0, seed=23)
+    rows = torch.zeros(R, d, dtype=torch.bfloat16, device="cuda")
+    assert rows.numel() > 2 ** 31
+    rows[R - 12:] = y
+    near = torch.arange(12, dtype=torch.int32, device="cuda").view(4, 3)
+    want, wdy = mz.combine_backward(dout, x, y, near, gate)
+    got, dy = mz.combine_backward(dout, x, rows, (near + (R - 12)).contiguous(), gate)
+    assert torch.equal(got, want) and torch.equal(dy[R - 12:], wdy)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_past_32_bit_offsets(bits):
+    """A tensor of 2^31 + 3000 elements whose last 4096 are those of a small one."""
+    n, m = 2 ** 31 + 3000, 4096
+    start = n // 256 * 256 - m + 256      # a block's start, so that both share their blocks
+    m = n - start
+    (w,), (g,) = adam_case([m], torch.bfloat16, torch.bfloat16, seed=24)
+    big, bg = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    big[start:], bg[start:] = w, g
+    for opt, gr in ((mz.AdamW([w], **HYPER, state_bits=bits), g), (mz.AdamW([big], **HYPER, state_bits=bits), bg)):
+        opt.step([gr])
+        opt.step([gr])
+    assert torch.equal(big[start:], w)
+    assert not big[:start].any()
 
 
 def test_route_logits():

@@ -139,6 +139,14 @@ def test_bias_follows_the_load():
     assert np.array_equal(b.cpu().numpy(), twin.step(r.counts.sum(0).cpu().numpy(), 128))
 
 
+def test_a_batch_without_tokens():
+    W_r, b, Wg, Wu, Wd, x, dout = layer(4, 2, 2, 256, 128, 0)
+    st = learn.RouterStep(4, 2, 2, W_r, b, Wg, Wu, Wd, lr=1e-2)
+    assert st.forward(x).shape == (0, 256)
+    g = st.backward(dout)
+    assert (g.W_r == 0).all() and (g.balance.loss == 0).all()
+
+
 def test_backward_needs_a_forward():
     W_r, b, Wg, Wu, Wd, x, dout = layer(2, 1, 1, 256, 128, 4)
     st = learn.RouterStep(2, 1, 1, W_r, b, Wg, Wu, Wd, lr=1e-2)
