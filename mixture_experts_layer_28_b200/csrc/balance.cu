@@ -171,36 +171,43 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
 }
 
 // Partial sums added up: a cluster of CTAs per sequence (one wherever E <= 128),
-// each CTA 128 experts; thread (y, x) adds rows y, y + RG, ... of experts 4 x ..
-// 4 x + 3, then the RG sums are added in order, so that a few hundred rows are
-// a few loads deep instead of one long chain (one CTA per sequence walking all
-// rows took 121 us for 4 sequences of 4096 tokens, E = 768; this 4.6 us).  The
-// CTAs' parts of the loss meet in the first one's shared memory.
-template <int RG, bool VEC>
-__global__ void __launch_bounds__(RG * 32)
+// each CTA 128 experts.  Lane x of a group of X lanes (X = 32, or the power of
+// two that covers a row of fewer than 128) takes experts 4 x .. 4 x + 3, group g
+// of the CTA's G = threads / X adds rows g, g + G, ...; the groups of a warp are
+// added by shuffles, the warps in order, so that a few hundred rows are a load or
+// two deep instead of one long chain (one CTA per sequence walking all rows took
+// 121 us for 4 sequences of 4096 tokens, E = 768; this 5).  The CTAs' parts of the
+// loss meet in the first one's shared memory.
+template <int WARPS, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32)
 balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcnt,
                      const int* __restrict__ pn, const int* __restrict__ seq,
                      const float* __restrict__ weight, int64_t T, int E, int K, int chunk, int nc,
-                     float* __restrict__ loss, int* __restrict__ counts, float* __restrict__ prob,
-                     float* __restrict__ coef) {
-  __shared__ float4 sum_s[RG][32];
-  __shared__ int4 cnt_s[RG][32];
+                     int X, float* __restrict__ loss, int* __restrict__ counts,
+                     float* __restrict__ prob, float* __restrict__ coef) {
+  __shared__ float4 sum_s[WARPS][32];
+  __shared__ int4 cnt_s[WARPS][32];
+  __shared__ int n_s[WARPS];
   __shared__ float part[4];          // warps 0..3: their experts' part of the loss
   __shared__ float cta_part[8];      // (first CTA) the CTAs' parts
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = lane & (X - 1), g = threadIdx.x / X, G = WARPS * 32 / X;
   const int s = blockIdx.x / nc, rank = blockIdx.x % nc;
   // (seq was complete before the partial sums' kernel let this one start)
   const int64_t a = seq_at(seq, s, T), e = seq_at(seq, s + 1, T);
+  const int64_t b0 = a / chunk, b1 = a < e ? (e - 1) / chunk + 1 : b0;
+  const int64_t r0 = b0 + s;                     // this sequence's slots
+  const int rows = static_cast<int>(b1 - b0);
+  const int j0 = rank * 128 + 4 * x;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t b0 = a / chunk, b1 = a < e ? (e - 1) / chunk + 1 : b0;
-  const int64_t r0 = b0 + s, rows = b1 - b0;     // this sequence's slots
-  const int j0 = rank * 128 + 4 * x;
   float v[4] = {0.f, 0.f, 0.f, 0.f};
   int c[4] = {0, 0, 0, 0};
+  int nt = 0;                                    // counted tokens
+  for (int r = threadIdx.x; r < rows; r += WARPS * 32) nt += pn[r0 + r];
   if (j0 < E) {
 #pragma unroll 4
-    for (int64_t r = y; r < rows; r += RG) {
+    for (int r = g; r < rows; r += G) {
       const float* ps = psum + (r0 + r) * E + j0;
       const int* pc = pcnt + (r0 + r) * E + j0;
       if (VEC) {
@@ -218,14 +225,24 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
       }
     }
   }
-  sum_s[y][x] = make_float4(v[0], v[1], v[2], v[3]);
-  cnt_s[y][x] = make_int4(c[0], c[1], c[2], c[3]);
-  int nt = 0;                                    // counted tokens
-  if (y < 4)
-    for (int64_t r = x; r < rows; r += 32) nt += pn[r0 + r];
+  for (int o = 16; o >= X; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      c[i] += __shfl_xor_sync(0xffffffffu, c[i], o);
+    }
+  }
+  nt = __reduce_add_sync(0xffffffffu, nt);
+  if (lane < X) {
+    sum_s[warp][lane] = make_float4(v[0], v[1], v[2], v[3]);
+    cnt_s[warp][lane] = make_int4(c[0], c[1], c[2], c[3]);
+  }
+  if (lane == 0) n_s[warp] = nt;
   __syncthreads();
-  if (y < 4) {
-    const int n = __reduce_add_sync(0xffffffffu, nt);
+  if (warp < 4) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) n += n_s[w];
     const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
     const int j = rank * 128 + threadIdx.x;
     float mine = 0.f;
@@ -233,9 +250,9 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
       float sum = 0.f;
       int cn = 0;
 #pragma unroll
-      for (int g = 0; g < RG; ++g) {
-        sum += reinterpret_cast<const float*>(sum_s[g])[threadIdx.x];
-        cn += reinterpret_cast<const int*>(cnt_s[g])[threadIdx.x];
+      for (int w = 0; w < WARPS; ++w) {
+        sum += reinterpret_cast<const float*>(sum_s[w])[threadIdx.x];
+        cn += reinterpret_cast<const int*>(cnt_s[w])[threadIdx.x];
       }
       const int64_t o = static_cast<int64_t>(s) * E + j;
       const float P = sum * inv;
@@ -247,12 +264,16 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
       mine = f * P;
     }
     mine = warp_sum(mine);
-    if (x == 0) part[y] = mine;
+    if (lane == 0) part[warp] = mine;
   }
   __syncthreads();
+  const float mine = part[0] + part[1] + part[2] + part[3];
+  if (nc == 1) {
+    if (threadIdx.x == 0) loss[s] = mine;
+    return;
+  }
   if (threadIdx.x == 0)
-    st_cluster_u32(mapa_shared(smem_u32(&cta_part[rank]), 0),
-                   __float_as_uint(part[0] + part[1] + part[2] + part[3]));
+    st_cluster_u32(mapa_shared(smem_u32(&cta_part[rank]), 0), __float_as_uint(mine));
   cluster_sync_all();
   if (rank == 0 && threadIdx.x == 0) {
     float l = 0.f;
@@ -415,16 +436,20 @@ cudaError_t launch_balance_loss(const float* logits, const float* offset, const 
     });
     if (e != cudaSuccess) return e;
   }
-  // row groups: 32 where a sequence has many rows to add, 8 for short ones
-  int nc = 1;
+  // 32 warps where a sequence has many rows to add, 8 for short ones
+  int nc = 1, X = 1;
   while (nc * 128 < E) nc *= 2;
-  const bool many = (pl.blocks + S) / S > 16;
-  auto final_stage = [&](auto rg, auto vec) {
-    constexpr auto kern = balance_final_kernel<decltype(rg)::value, decltype(vec)::value != 0>;
-    return launch_pdl_cluster(kern, nc, dim3(static_cast<unsigned>(S) * nc),
-                              dim3(decltype(rg)::value * 32), 0, stream, psum, pcnt, pn, seq,
-                              weight, T, E, K, pl.chunk, nc, loss, counts, prob, coef);
+  while (X < 32 && 4 * X < E) X *= 2;
+  auto final_stage = [&](auto warps, auto vec) {
+    constexpr auto kern = balance_final_kernel<decltype(warps)::value, decltype(vec)::value != 0>;
+    const dim3 grid(static_cast<unsigned>(S) * nc), block(decltype(warps)::value * 32);
+    if (nc == 1)
+      return launch_pdl(kern, grid, block, 0, stream, psum, pcnt, pn, seq, weight, T, E, K,
+                        pl.chunk, nc, X, loss, counts, prob, coef);
+    return launch_pdl_cluster(kern, nc, grid, block, 0, stream, psum, pcnt, pn, seq, weight, T, E,
+                              K, pl.chunk, nc, X, loss, counts, prob, coef);
   };
+  const bool many = (pl.blocks + S) / S > 16;
   if (E % 4 == 0)
     return many ? final_stage(IntC<32>{}, IntC<1>{}) : final_stage(IntC<8>{}, IntC<1>{});
   return many ? final_stage(IntC<32>{}, IntC<0>{}) : final_stage(IntC<8>{}, IntC<0>{});
