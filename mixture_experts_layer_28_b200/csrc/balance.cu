@@ -197,6 +197,7 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int x = lane & (X - 1), g = threadIdx.x / X, G = WARPS * 32 / X;
   const int s = blockIdx.x / nc, rank = blockIdx.x % nc;
+  if (nc > 1) cluster_begun_arrive();
   // (seq was complete before the partial sums' kernel let this one start)
   const int64_t a = seq_at(seq, s, T), e = seq_at(seq, s + 1, T);
   const int64_t b0 = a / chunk, b1 = a < e ? (e - 1) / chunk + 1 : b0;
@@ -276,6 +277,7 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
     if (threadIdx.x == 0) loss[s] = mine;
     return;
   }
+  cluster_begun_wait();
   if (threadIdx.x == 0)
     st_cluster_u32(mapa_shared(smem_u32(&cta_part[rank]), 0), __float_as_uint(mine));
   cluster_sync_all();

@@ -68,6 +68,7 @@ combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict_
   const int part = CUT ? blockIdx.x % parts : 0;
   const int c0 = CUT ? static_cast<int>(static_cast<int64_t>(d8) * part / parts) : 0;
   const int c1 = CUT ? static_cast<int>(static_cast<int64_t>(d8) * (part + 1) / parts) : d8;
+  if (CUT) cluster_begun_arrive();
   griddep_wait();
   int s = -1;   // (warp 0) this lane's pick
   if (warp == 0) {
@@ -83,6 +84,7 @@ combine_backward_kernel(const uint4* __restrict__ dout, const uint4* __restrict_
     }
     if (lane == 0) nffn = __popc(m);
   }
+  if (CUT) cluster_begun_wait();
   __syncthreads();
   const int n = nffn;
   const bool zero = n < K;

@@ -6,6 +6,16 @@
 
 namespace moezc {
 
+// A CTA's shared memory may be written by its cluster's others once it has
+// begun: each arrives as its first step and waits before its first such store,
+// by when the others have long arrived (all threads, each warp converged).
+__device__ __forceinline__ void cluster_begun_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_begun_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // launch_pdl as clusters of `cluster` CTAs along x (a divisor of the grid).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), unsigned cluster, dim3 grid,
