@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from typing import NamedTuple, Optional, Sequence
 
@@ -537,6 +538,9 @@ class Moment8(NamedTuple):
     scales: torch.Tensor
 
 
+_SHAPE, _DTYPE = operator.attrgetter("shape"), operator.attrgetter("dtype")
+
+
 class AdamW:
     """AdamW over many tensors at once (moe_zc_adamw).
 
@@ -547,13 +551,14 @@ class AdamW:
     for fresh ones.  master: fp32 weights, one per bf16 parameter, or True to
     make them from params.  step: the steps done so far; the count lives on
     the device (step_count), so a step captured into a CUDA graph goes on
-    counting in its replays.
+    counting in its replays.  Steps write the storages that these tensors have
+    now: load into them (copy_) instead of giving them other ones.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float, betas=(0.9, 0.95),
                  eps: float = 1e-8, weight_decay: float = 0.1, state_bits: int = 32,
                  exp_avg=None, exp_avg_sq=None, master=None, step: int = 0):
-        self.params = list(params)
+        self.params = tuple(params)
         if not self.params:
             raise ValueError("params is empty")
         if state_bits not in (8, 32):
@@ -571,7 +576,7 @@ class AdamW:
             raise ValueError("master weights go with bf16 params")
         self.exp_avg = self._states(exp_avg, eight)
         self.exp_avg_sq = self._states(exp_avg_sq, eight)
-        self.master = list(master) if master is not None else None
+        self.master = tuple(master) if master is not None else None
         for name in ("exp_avg", "exp_avg_sq", "master"):
             v = getattr(self, name)
             if v is not None and len(v) != len(self.params):
@@ -581,16 +586,19 @@ class AdamW:
         self._table = np.zeros(len(self.params), dtype=_ADAMW_TENSOR)
         self._table["n"] = n
         dev = p0.get_device()
-        spans = []   # what the step writes
+        spans = []        # what the step writes
+        self._held = []   # ... its storages, whatever .data the caller sets later
 
         def put(field, tensors, dtype, shapes, name):
             ptrs = []
             for i, (t, shape) in enumerate(zip(tensors, shapes)):
-                ptrs.append(_arg(t, dtype, shape, (name, i), dev))
+                ptrs.append(_arg(t, dtype, shape, f"{name}[{i}]", dev))
+                self._held.append(t.detach())
                 spans.append((ptrs[-1], ptrs[-1] + t.numel() * t.element_size()))
             self._table[field] = ptrs
+            return ptrs
 
-        put("param", self.params, p0.dtype, self._shapes, "params")
+        self._param_ptrs = put("param", self.params, p0.dtype, self._shapes, "params")
         for field in ("exp_avg", "exp_avg_sq"):
             v = getattr(self, field)
             if eight:
@@ -612,12 +620,22 @@ class AdamW:
 
     def _states(self, given, eight):
         if given is not None:
-            return list(given)
+            return tuple(given)
         if not eight:
-            return [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
-        return [Moment8(torch.zeros_like(p, dtype=torch.uint8),
-                        torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device))
-                for p in self.params]
+            return tuple(torch.zeros_like(p, dtype=torch.float32) for p in self.params)
+        return tuple(Moment8(torch.zeros_like(p, dtype=torch.uint8),
+                             torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device))
+                     for p in self.params)
+
+    def _fit(self, grads, dtype, dev, shapes=None) -> bool:
+        # (maps: a fifth less host time than a loop over the tensors)
+        try:
+            return (list(map(_SHAPE, grads)) == (shapes or self._shapes)
+                    and set(map(_DTYPE, grads)) == {dtype}
+                    and set(map(torch.Tensor.get_device, grads)) == {dev}
+                    and all(map(torch.Tensor.is_contiguous, grads)))
+        except (AttributeError, TypeError):   # not a tensor
+            return False
 
     def step(self, grads: Sequence[torch.Tensor], lr_scale: Optional[torch.Tensor] = None,
              grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -626,18 +644,20 @@ class AdamW:
         (a schedule's and a clipping factor), read when the step runs."""
         if len(grads) != len(self.params):
             raise ValueError("grads must hold one tensor per parameter")
-        gt = grads[0].dtype
+        gt = getattr(grads[0], "dtype", None)
         if gt not in (torch.float32, torch.bfloat16):
             raise ValueError(f"grads must be torch.float32 or torch.bfloat16, got {gt}")
         dev = _current_device()
         if self.device.index != dev:
             raise ValueError(f"the current CUDA device must be {self.device}")
-        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
-            if (g.dtype is not gt or g.shape != shape or g.get_device() != dev
-                    or not g.is_contiguous()):
-                raise ValueError(f"grads[{i}] must be a contiguous {gt} tensor of shape "
-                                 f"{tuple(shape)} on {self.device}")
-        self._table["grad"] = [g.data_ptr() for g in grads]
+        if not self._fit(grads, gt, dev):
+            for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+                if not self._fit([g], gt, dev, [shape]):
+                    raise ValueError(f"grads[{i}] must be a contiguous {gt} tensor of shape "
+                                     f"{tuple(shape)} on {self.device}")
+        if list(map(torch.Tensor.data_ptr, self.params)) != self._param_ptrs:
+            raise ValueError("a parameter was given another storage since this AdamW was made")
+        self._table["grad"] = list(map(torch.Tensor.data_ptr, grads))
         self.args.grad_type = BF16 if gt == torch.bfloat16 else F32
         scales = [None if t is None else _arg(t.view(-1), torch.float32, (1,), name, dev)
                   for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale"))]

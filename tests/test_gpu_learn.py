@@ -647,3 +647,41 @@ def test_route_logits():
             p = ref.softmax64(logits.cpu(), None if o is None else o.cpu())
             assert torch.allclose(p.gather(1, idx.cpu().long()), gate.cpu().double(), rtol=1e-5)
     mz.synchronize()
+
+
+def test_adamw_refuses_a_parameter_with_another_storage():
+    params, grads = adam_case([300, 70], torch.float32, torch.float32)
+    opt = mz.AdamW(params, **HYPER)
+    opt.step(grads)
+    old = params[1].data
+    want = old.clone()
+    params[1].data = torch.ones(70, device="cuda")
+    with pytest.raises(ValueError, match="another storage"):
+        opt.step(grads)
+    assert torch.equal(old, want) and (params[1] == 1).all()
+    assert opt.step_count.tolist() == [1, 0]
+    params[1].data = old
+    opt.step(grads)
+    assert opt.step_count.tolist() == [2, 0]
+
+
+def test_adamw_refuses_missing_gradients():
+    params, grads = adam_case([300, 70], torch.float32, torch.float32)
+    opt = mz.AdamW(params, **HYPER)
+    for bad in ([None, grads[1]], [grads[0], None], grads[:1]):
+        with pytest.raises(ValueError):
+            opt.step(bad)
+    assert opt.step_count.tolist() == [0, 0]
+
+
+def test_adamw_keeps_its_states_storages():
+    # a state whose .data is set elsewhere: the step still writes memory it holds
+    params, grads = adam_case([4096], torch.float32, torch.float32)
+    opt, twin = (mz.AdamW([p], **HYPER) for p in (params[0], params[0].clone()))
+    opt.exp_avg[0].data = torch.empty(0, device="cuda")
+    others = [torch.full((4096,), 7.0, device="cuda") for _ in range(4)]   # would take a freed one's place
+    for _ in range(2):
+        opt.step(grads)
+        twin.step(grads)
+    assert torch.equal(opt.params[0], twin.params[0])
+    assert all((o == 7).all() for o in others)

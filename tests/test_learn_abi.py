@@ -184,3 +184,8 @@ def test_adamw_refuses_at_construction():
         mz.AdamW([p], 1e-3, step=-1)
     with pytest.raises(ValueError, match="CUDA device"):
         mz.AdamW([p], 1e-3)
+
+
+def test_adamw_names_the_tensor():
+    with pytest.raises(ValueError, match=r"^params\[0\] must be on the current CUDA device$"):
+        mz.AdamW([torch.zeros(4)], 1e-3)
