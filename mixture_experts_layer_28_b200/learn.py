@@ -62,7 +62,8 @@ class RouterStep:
                 seq_start: Optional[torch.Tensor] = None,
                 logit_offset: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The layer's output for x bf16 [T, d]; mask and seq_start as for
-        balance_loss.  Keeps what backward needs."""
+        balance_loss (what padding holds reaches its own output rows alone).
+        Keeps what backward needs."""
         logits, idx, gate, zsum, counts = mz.route_logits(x, self.W_r, self.b, self.N, self.Z,
                                                           self.K, logit_offset)
         rows = int(counts[: self.N].sum())          # the one host read-back
@@ -84,6 +85,8 @@ class RouterStep:
         dloss = torch.full((S,), self.balance / max(S, 1), device=x.device)
         dlogits = mz.route_backward(logits, idx, dgate, r.coef, dloss, off, mask, seq_start,
                                     dtype=torch.bfloat16)
+        if mask is not None:   # (a product with 0 would still carry padding's NaN)
+            x = x.masked_fill((mask == 0).unsqueeze(1), 0)
         return RouterGrad(dlogits.t() @ x, r)
 
     def step(self, grad: torch.Tensor, lr_scale: Optional[torch.Tensor] = None,

@@ -154,3 +154,52 @@ def test_backward_needs_a_forward():
         st.backward(dout)
     with pytest.raises(ValueError):
         learn.RouterStep(0, 3, 1, W_r, b, Wg, Wu, Wd, lr=1e-2)
+
+
+@pytest.mark.parametrize("mask_type", [torch.bool, torch.uint8])
+def test_padding_may_hold_anything(mask_type):
+    """NaN in padding reaches its own output rows alone.  Without a bias both a
+    row of NaN and one of zeros pick experts 0 .. K - 1, so the rest of the step
+    is the same, bits included."""
+    N, Z, K, T, d = 6, 3, 3, 90, 256
+    W_r, b, Wg, Wu, Wd, x, dout = layer(N, Z, K, d, 128, T, seed=11)
+    b.zero_()
+    mask = (torch.arange(T) % 4 != 1).to(mask_type).cuda()
+    got = []
+    for fill in (0.0, float("nan")):
+        x[mask == 0], dout[mask == 0] = fill, fill
+        st = learn.RouterStep(N, Z, K, W_r, b, Wg, Wu, Wd, lr=1e-2)
+        out = st.forward(x, mask)
+        got.append((out[mask != 0], *st.backward(dout)))
+    (o0, w0, r0), (o1, w1, r1) = got
+    assert torch.isfinite(w1).all() and torch.equal(w0, w1) and torch.equal(o0, o1)
+    for a, c in zip(r0, r1):
+        assert torch.equal(a, c)
+
+
+def test_all_picks_on_zero_experts():
+    N, Z, K, T, d = 4, 5, 3, 40, 256
+    W_r, b, Wg, Wu, Wd, x, dout = layer(N, Z, K, d, 128, T, seed=3)
+    b[:N] = -10.0
+    st = learn.RouterStep(N, Z, K, W_r, b, Wg, Wu, Wd, lr=1e-2)
+    out = st.forward(x)
+    idx, slot = st._saved[2], st._saved[4]
+    assert (idx >= N).all() and (slot < 0).all()
+    assert torch.equal(out, mz.forward(x, W_r, b, Wg, Wu, Wd, N, Z, K))
+    g = st.backward(dout)
+    assert g.balance.counts[0, :N].sum() == 0 and g.balance.counts.sum() == T * K
+    # the gates' gradient is dout . x for every pick: with p the softmax,
+    # dlogits_i = p_i (x . dout) ([i picked] - sum of the picks' p), and the loss's
+    W = W_r.double().cpu()
+    xc, dc = x.double().cpu(), dout.double().cpu()
+    p = torch.softmax(xc @ W.t(), 1)
+    on = torch.zeros(T, N + Z, dtype=torch.float64).scatter_(1, idx.long().cpu(), 1.0)
+    a = on * (xc * dc).sum(1, keepdim=True) + 1e-2 * g.balance.coef.double().cpu()
+    want = (p * (a - (p * a).sum(1, keepdim=True))).t() @ xc
+    # roundings: the logits' fp32 sums (d terms) move p by d U |x| |W| relative,
+    # dgate's the same way; dlogits and the product are rounded to bf16
+    dl = p * ((a.abs() + (p * a.abs()).sum(1, keepdim=True)))
+    rel = 4 * d * U * (1 + (xc.abs() @ W.abs().t()).max())
+    err = ((UB + rel) * dl).t() @ xc.abs() + p.t() @ (xc.abs() * 4 * d * U * (xc * dc).abs().sum(1, keepdim=True)) * 2
+    err = err + UB * want.abs() + T * U * (dl.t() @ xc.abs())
+    assert ((g.W_r.double().cpu() - want).abs() <= err).all()
