@@ -324,7 +324,7 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
   // tokens [sa, se) share s (S: no sequence); none known yet
   int s = S;
   int64_t sa = 0, se = coef ? 0 : T;
-  Row<NV> dc;        // dloss_s coef_s of the sequence (0: none)
+  Row<NV> dc;        // dloss_s coef_s of the sequence, up to a constant (0: none)
   dc.fill(0.f);
   unsigned bits = 0;
   int left = 0;
@@ -347,12 +347,17 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
       }
       dc.fill(0.f);
       if (s < S) {
-        row_load<NV, KIND>(dc, coef + static_cast<int64_t>(s) * E, E, lane, 0.f);
-        const F2 dl = both(dloss[s]);
+        // Less the coefficient of least magnitude: what all have in common cancels
+        // in p (a - sum p a), but only up to the roundings of p, and under an
+        // even load nearly all of a coefficient is common.  (Past E, where p is 0,
+        // stands the first one.)
+        const float* cs = coef + static_cast<int64_t>(s) * E;
+        row_load<NV, KIND>(dc, cs, E, lane, cs[0]);
+        const F2 dl = both(dloss[s]), least = both(-row_least(dc));
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) dc.v[i][h] = mul2(dc.v[i][h], dl);
+          for (int h = 0; h < 2; ++h) dc.v[i][h] = mul2(add2(dc.v[i][h], least), dl);
       }
     }
     fetch();

@@ -186,6 +186,24 @@ __device__ __forceinline__ float row_lane_sum(const Row<NV>& r) {
   return a.x + a.y;
 }
 
+// A row's value of least magnitude, 0 where its values differ in sign (a NaN is
+// passed over; what stands past E counts).
+template <int NV>
+__device__ __forceinline__ float row_least(const Row<NV>& r) {
+  float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 a = up(r.v[i][h]);
+      asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(a.x), "f"(a.y));
+      asm("max.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(a.x), "f"(a.y));
+    }
+  asm("redux.sync.min.f32 %0, %0, 0xffffffff;" : "+f"(lo));
+  hi = warp_max(hi);
+  return lo >= 0.f ? lo : hi <= 0.f ? hi : 0.f;
+}
+
 // A warp's rows on their way to it: a ring of DEPTH stages in shared memory,
 // each a row and two arrays of up to 32 words, filled by asynchronous copies.
 // Each lane reads back only what it copied itself, so waiting for its own

@@ -183,6 +183,33 @@ def test_route_backward(E, K, dtype, what):
     assert ((got.cpu().double() - want).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("E", [4, 6, 12, 130, 768, 1021])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_gradient_near_an_even_load(E, sign):
+    """The softmax's gradient does not see what all coefficients have in common,
+    so its error goes by what is left: nothing where all are equal."""
+    T = 40
+    logits, _ = rows_case(T, E, 1, seed=E)
+    seq, dloss = ints([0, 13, 40]), torch.tensor([0.7, -1.3]).cuda()
+    same = torch.full((2, E), 0.3 * sign).cuda()
+    assert (mz.route_backward(logits, coef=same, dloss=dloss, seq_start=seq) == 0).all()
+    coef = same + 1e-4 * torch.rand(2, E, generator=gen(E)).cuda()
+    got = mz.route_backward(logits, coef=coef, dloss=dloss, seq_start=seq)
+    least = coef.abs().min(1, keepdim=True).values * sign
+    want, size = ref.route_backward(logits, coef=coef.double() - least.double(), dloss=dloss, seq=seq)
+    bound = (2 * ref.softmax_steps(logits.cpu()) + E + 40) * U * size
+    assert ((got.cpu().double() - want).abs() <= bound).all()
+
+
+def test_an_even_load_has_no_gradient():
+    # K == E: every expert is picked by every token
+    for E in (1, 4, 6, 32):
+        logits, idx = rows_case(50, E, E, seed=E)
+        seq = ints([0, 20, 50])
+        r = mz.balance_loss(logits, idx, seq_start=seq)
+        assert (mz.route_backward(logits, idx, coef=r.coef, dloss=torch.ones(2, device="cuda"), seq_start=seq) == 0).all()
+
+
 @pytest.mark.parametrize("T", [0, 1, 3, 8, 20000])
 def test_route_backward_lengths(T):
     logits, idx = rows_case(min(T, 50), 16, 2, seed=T)
