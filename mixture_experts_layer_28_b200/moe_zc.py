@@ -7,6 +7,7 @@ the call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import operator
@@ -585,6 +586,7 @@ class AdamW:
         n = [p.numel() for p in self.params]
         self._table = np.zeros(len(self.params), dtype=_ADAMW_TENSOR)
         self._table["n"] = n
+        self._table_ptr = self._table.ctypes.data
         dev = p0.get_device()
         spans = []        # what the step writes
         self._held = []   # ... its storages, whatever .data the caller sets later
@@ -657,11 +659,11 @@ class AdamW:
                                      f"{tuple(shape)} on {self.device}")
         if list(map(torch.Tensor.data_ptr, self.params)) != self._param_ptrs:
             raise ValueError("a parameter was given another storage since this AdamW was made")
-        self._table["grad"] = list(map(torch.Tensor.data_ptr, grads))
+        self._table["grad"] = array.array("Q", map(torch.Tensor.data_ptr, grads))
         self.args.grad_type = BF16 if gt == torch.bfloat16 else F32
         scales = [None if t is None else _arg(t.view(-1), torch.float32, (1,), name, dev)
                   for t, name in ((lr_scale, "lr_scale"), (grad_scale, "grad_scale"))]
-        _check(lib().moe_zc_adamw(self._table.ctypes.data, len(grads), ctypes.byref(self.args),
+        _check(lib().moe_zc_adamw(self._table_ptr, len(grads), ctypes.byref(self.args),
                                   self.step_count.data_ptr(), *scales, _stream_of(stream, dev)),
                "moe_zc_adamw")
 
