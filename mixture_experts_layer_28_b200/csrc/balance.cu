@@ -400,21 +400,20 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
     }
     // with e = exp(l - max): p = e / sum e, sum_j p_j a_j = (sum_j e_j a_j) / sum e
     row_exp<NV, KIND>(p, off, E, lane);
-    F2 ea = mul2(p.v[0][0], a.v[0][0]);
+    F2 ea[2] = {mul2(p.v[0][0], a.v[0][0]), mul2(p.v[0][1], a.v[0][1])};
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 1; i < NV; ++i)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (i + h > 0) ea = fma2(p.v[i][h], a.v[i][h], ea);
-    const float2 ea2 = up(ea);
+      for (int h = 0; h < 2; ++h) ea[h] = fma2(p.v[i][h], a.v[i][h], ea[h]);
+    const float2 ea2 = up(add2(ea[0], ea[1]));
     const float2 sums = up(warp_sum2(pk(row_lane_sum(p), ea2.x + ea2.y)));
     const float inv = rcp_approx(sums.x);
-    const F2 inv2 = both(inv), dot = both(-sums.y * inv);
+    const F2 inv2 = both(inv), dot = both(-sums.y * inv * inv);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        a.v[i][h] = mul2(mul2(p.v[i][h], inv2), add2(a.v[i][h], dot));
+        a.v[i][h] = mul2(p.v[i][h], fma2(a.v[i][h], inv2, dot));
     row_store<NV, KIND>(a, dlogits + t * E, E, lane);
   }
   ring.drain();

@@ -148,15 +148,15 @@ template <int NV, int KIND>
 __device__ __forceinline__ void row_exp(Row<NV>& r, const Offset<NV, KIND>& offset, int E,
                                         int lane) {
   offset.add(r, E, lane);
-  float m = -INFINITY;
+  float m2[2] = {-INFINITY, -INFINITY};   // (two chains)
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float2 a = up(r.v[i][h]);
-      m = fmaxf(m, fmaxf(a.x, a.y));
+      asm("max.f32 %0, %0, %1, %2;" : "+f"(m2[h]) : "f"(a.x), "f"(a.y));
     }
-  m = warp_max(m);
+  float m = warp_max(fmaxf(m2[0], m2[1]));
   if (!(fabsf(m) < 1e37f)) {   // (its product with log2 e might overflow: subtract first)
     const F2 neg = both(-m);
 #pragma unroll
@@ -179,10 +179,13 @@ __device__ __forceinline__ void row_exp(Row<NV>& r, const Offset<NV, KIND>& offs
 // This lane's part of a row's sum.
 template <int NV>
 __device__ __forceinline__ float row_lane_sum(const Row<NV>& r) {
-  F2 s = add2(r.v[0][0], r.v[0][1]);
+  F2 s = r.v[0][0], t = r.v[0][1];
 #pragma unroll
-  for (int i = 1; i < NV; ++i) s = add2(s, add2(r.v[i][0], r.v[i][1]));
-  const float2 a = up(s);
+  for (int i = 1; i < NV; ++i) {
+    s = add2(s, r.v[i][0]);
+    t = add2(t, r.v[i][1]);
+  }
+  const float2 a = up(add2(s, t));
   return a.x + a.y;
 }
 
