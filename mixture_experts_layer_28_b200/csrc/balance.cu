@@ -174,36 +174,42 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
   ring.drain();
 }
 
-// Partial sums added up: a cluster of CTAs per sequence (one wherever E <= 128),
-// each CTA 128 experts.  Lane x of a group of X lanes (X = 32, or the power of
-// two that covers a row of fewer than 128) takes experts 4 x .. 4 x + 3, group g
-// of the CTA's G = threads / X adds rows g, g + G, ...; the groups of a warp are
-// added by shuffles, the warps in order, so that a few hundred rows are a load or
-// two deep instead of one long chain (one CTA per sequence walking all rows took
-// 121 us for 4 sequences of 4096 tokens, E = 768; this 5).  The CTAs' parts of the
-// loss meet in the first one's shared memory.
-template <int WARPS, bool VEC>
+// Partial sums added up: a cluster of ne x nr CTAs per sequence, ne slices of 128
+// experts (the power of two that covers E) and nr parts of the rows (8 / ne where
+// there are many).  Lane x of a group of X lanes (X = 32, or the power of two that
+// covers a row of fewer than 128) takes experts 4 x .. 4 x + 3, group g of the
+// CTA's G = threads / X adds every G-th row of its part; the groups of a warp are
+// added by shuffles, the warps in order, the parts in order in the slice's first
+// CTA, so that a few hundred rows are a load or two deep instead of one long chain
+// (one CTA per sequence walking all rows took 121 us for 4 sequences of 4096
+// tokens, E = 768; this 5).  The slices' parts of the loss meet in the first CTA's
+// shared memory.
+template <int WARPS, bool VEC, bool PARTS>
 __global__ void __launch_bounds__(WARPS * 32)
 balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcnt,
                      const int* __restrict__ pn, const int* __restrict__ seq,
-                     const float* __restrict__ weight, int64_t T, int E, int K, int chunk, int nc,
-                     int X, float* __restrict__ loss, int* __restrict__ counts,
+                     const float* __restrict__ weight, int64_t T, int E, int K, int chunk, int ne,
+                     int nr, int X, float* __restrict__ loss, int* __restrict__ counts,
                      float* __restrict__ prob, float* __restrict__ coef) {
   __shared__ float4 sum_s[WARPS][32];
   __shared__ int4 cnt_s[WARPS][32];
   __shared__ int n_s[WARPS];
-  __shared__ float part[4];          // warps 0..3: their experts' part of the loss
-  __shared__ float cta_part[8];      // (first CTA) the CTAs' parts
+  __shared__ float part[4];            // warps 0..3: their experts' part of the loss
+  __shared__ float slice_part[8];      // (first CTA) the slices' parts
+  __shared__ float meet_sum[PARTS ? 8 : 1][128];   // (a slice's first CTA) the sums of its parts
+  __shared__ int meet_cnt[PARTS ? 8 : 1][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int x = lane & (X - 1), g = threadIdx.x / X, G = WARPS * 32 / X;
+  const int nc = ne * nr;
   const int s = blockIdx.x / nc, rank = blockIdx.x % nc;
+  const int slice = PARTS ? rank % ne : rank, rpart = PARTS ? rank / ne : 0;
   if (nc > 1) cluster_begun_arrive();
   // (seq was complete before the partial sums' kernel let this one start)
   const int64_t a = seq_at(seq, s, T), e = seq_at(seq, s + 1, T);
   const int64_t b0 = a / chunk, b1 = a < e ? (e - 1) / chunk + 1 : b0;
   const int64_t r0 = b0 + s;                     // this sequence's slots
   const int rows = static_cast<int>(b1 - b0);
-  const int j0 = rank * 128 + 4 * x;
+  const int j0 = slice * 128 + 4 * x;
   griddep_wait();
   griddep_launch_dependents();
   float v[4] = {0.f, 0.f, 0.f, 0.f};
@@ -212,7 +218,7 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
   for (int r = threadIdx.x; r < rows; r += WARPS * 32) nt += pn[r0 + r];
   if (j0 < E) {
 #pragma unroll 4
-    for (int r = g; r < rows; r += G) {
+    for (int r = rpart * G + g; r < rows; r += PARTS ? nr * G : G) {
       const float* ps = psum + (r0 + r) * E + j0;
       const int* pc = pcnt + (r0 + r) * E + j0;
       if (VEC) {
@@ -244,21 +250,38 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
   }
   if (lane == 0) n_s[warp] = nt;
   __syncthreads();
+  const int j = slice * 128 + threadIdx.x;
+  const bool mine = threadIdx.x < 128 && j < E;
+  float sum = 0.f, inv = 0.f;   // (inv: 1 / counted tokens, 0 for none)
+  int cn = 0;
   if (warp < 4) {
-    int n = 0;
+    const int n = __reduce_add_sync(0xffffffffu, lane < WARPS ? n_s[lane] : 0);
+    if (n > 0) inv = 1.0f / static_cast<float>(n);
+  }
+  if (mine) {
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) n += n_s[w];
-    const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.f;
-    const int j = rank * 128 + threadIdx.x;
-    float mine = 0.f;
-    if (j < E) {
-      float sum = 0.f;
-      int cn = 0;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        sum += reinterpret_cast<const float*>(sum_s[w])[threadIdx.x];
-        cn += reinterpret_cast<const int*>(cnt_s[w])[threadIdx.x];
+    for (int w = 0; w < WARPS; ++w) {
+      sum += reinterpret_cast<const float*>(sum_s[w])[threadIdx.x];
+      cn += reinterpret_cast<const int*>(cnt_s[w])[threadIdx.x];
+    }
+  }
+  if (PARTS) {
+    cluster_begun_wait();
+    if (mine) {
+      st_cluster_u32(mapa_shared(smem_u32(&meet_sum[rpart][threadIdx.x]), slice),
+                     __float_as_uint(sum));
+      st_cluster_u32(mapa_shared(smem_u32(&meet_cnt[rpart][threadIdx.x]), slice), cn);
+    }
+    cluster_sync_all();
+    if (mine && rpart == 0)
+      for (int q = 1; q < nr; ++q) {
+        sum += meet_sum[q][threadIdx.x];
+        cn += meet_cnt[q][threadIdx.x];
       }
+  }
+  if (rpart == 0 && warp < 4) {
+    float l = 0.f;
+    if (mine) {
       const int64_t o = static_cast<int64_t>(s) * E + j;
       const float P = sum * inv;
       const float w = weight ? weight[j] : static_cast<float>(E);
@@ -266,25 +289,25 @@ balance_final_kernel(const float* __restrict__ psum, const int* __restrict__ pcn
       counts[o] = cn;
       prob[o] = P;
       coef[o] = f * inv;
-      mine = f * P;
+      l = f * P;
     }
-    mine = warp_sum(mine);
-    if (lane == 0) part[warp] = mine;
+    l = warp_sum(l);
+    if (lane == 0) part[warp] = l;
   }
   __syncthreads();
-  const float mine = part[0] + part[1] + part[2] + part[3];
-  if (nc == 1) {
-    if (threadIdx.x == 0) loss[s] = mine;
+  const bool first = rpart == 0 && threadIdx.x == 0;
+  const float l = first ? part[0] + part[1] + part[2] + part[3] : 0.f;
+  if (ne == 1) {
+    if (first) loss[s] = l;
     return;
   }
-  cluster_begun_wait();
-  if (threadIdx.x == 0)
-    st_cluster_u32(mapa_shared(smem_u32(&cta_part[rank]), 0), __float_as_uint(mine));
+  if (!PARTS) cluster_begun_wait();
+  if (first) st_cluster_u32(mapa_shared(smem_u32(&slice_part[slice]), 0), __float_as_uint(l));
   cluster_sync_all();
   if (rank == 0 && threadIdx.x == 0) {
-    float l = 0.f;
-    for (int r = 0; r < nc; ++r) l += cta_part[r];
-    loss[s] = l;
+    float all = 0.f;
+    for (int q = 0; q < ne; ++q) all += slice_part[q];
+    loss[s] = all;
   }
 }
 
@@ -446,23 +469,31 @@ cudaError_t launch_balance_loss(const float* logits, const float* offset, const 
     });
     if (e != cudaSuccess) return e;
   }
-  // 32 warps where a sequence has many rows to add, 8 for short ones
-  int nc = 1, X = 1;
-  while (nc * 128 < E) nc *= 2;
+  // 8 warps where that leaves each group at most three of a sequence's rows, else
+  // 32; and where those still had more than one, parts of the rows (4096 x 96:
+  // 7.5 -> 6.0 us, 16384 x 96 11.7 -> 9.2, 8192 x 1024 in 16 sequences 16.0 -> 13.5)
+  int ne = 1, X = 1, nr = 1;
+  while (ne * 128 < E) ne *= 2;
   while (X < 32 && 4 * X < E) X *= 2;
-  auto final_stage = [&](auto warps, auto vec) {
-    constexpr auto kern = balance_final_kernel<decltype(warps)::value, decltype(vec)::value != 0>;
+  const int64_t rows = (pl.blocks + S) / S;
+  const bool many = rows > 3 * (256 / X);
+  while (many && ne * nr < 8 && rows > nr * (1024 / X)) nr *= 2;
+  const int nc = ne * nr;
+  auto final_stage = [&](auto warps, auto vec, auto parts) {
+    constexpr auto kern = balance_final_kernel<decltype(warps)::value, decltype(vec)::value != 0,
+                                               decltype(parts)::value != 0>;
     const dim3 grid(static_cast<unsigned>(S) * nc), block(decltype(warps)::value * 32);
     if (nc == 1)
       return launch_pdl(kern, grid, block, 0, stream, psum, pcnt, pn, seq, weight, T, E, K,
-                        pl.chunk, nc, X, loss, counts, prob, coef);
+                        pl.chunk, ne, nr, X, loss, counts, prob, coef);
     return launch_pdl_cluster(kern, nc, grid, block, 0, stream, psum, pcnt, pn, seq, weight, T, E,
-                              K, pl.chunk, nc, X, loss, counts, prob, coef);
+                              K, pl.chunk, ne, nr, X, loss, counts, prob, coef);
   };
-  const bool many = (pl.blocks + S) / S > 16;
-  if (E % 4 == 0)
-    return many ? final_stage(IntC<32>{}, IntC<1>{}) : final_stage(IntC<8>{}, IntC<1>{});
-  return many ? final_stage(IntC<32>{}, IntC<0>{}) : final_stage(IntC<8>{}, IntC<0>{});
+  auto with_vec = [&](auto vec) {
+    if (!many) return final_stage(IntC<8>{}, vec, IntC<0>{});
+    return nr > 1 ? final_stage(IntC<32>{}, vec, IntC<1>{}) : final_stage(IntC<32>{}, vec, IntC<0>{});
+  };
+  return E % 4 == 0 ? with_vec(IntC<1>{}) : with_vec(IntC<0>{});
 }
 
 template <typename OUT>
