@@ -28,7 +28,6 @@
 namespace moezc {
 namespace {
 
-constexpr int BAL_WARPS = 8;
 constexpr int BAL_THREADS = BAL_WARPS * 32;
 
 // Offset s of the sequences, inside [0, T] whatever the caller's array holds.
@@ -75,29 +74,29 @@ __device__ __forceinline__ int seq_of(const int* __restrict__ seq, int S, int64_
   return lo;
 }
 
-// Which of a warp's next 32 tokens (t, t + BAL_WARPS, ... below end) are not
-// masked, as bits.
+// Which of a warp's next 32 tokens (t, t + W, ... below end) are not masked, as bits.
+template <int W>
 __device__ __forceinline__ unsigned on_bits(const uint8_t* __restrict__ mask, int64_t t,
                                             int64_t end, int lane) {
-  const int64_t u = t + static_cast<int64_t>(lane) * BAL_WARPS;
+  const int64_t u = t + static_cast<int64_t>(lane) * W;
   return __ballot_sync(0xffffffffu, !mask || (u < end && mask[u]));
 }
 
 // Partial sums of one (block, sequence) pair: block b's tokens of sequence s
 // go to slot b + s.  Walking the tokens, each step ends a block or a sequence,
 // so no two pairs share a slot and blocks + sequences slots are enough.  Warp w
-// takes tokens w, w + BAL_WARPS, ... of the block's range.
-template <int NV, int KIND>
-__global__ void __launch_bounds__(BAL_THREADS, bal_blocks(NV))
+// takes tokens w, w + W, ... of the block's range.
+template <int NV, int KIND, int W>
+__global__ void __launch_bounds__(W * 32, W == BAL_WARPS ? bal_blocks(NV) : 1)
 balance_partial_kernel(const float* __restrict__ logits, const float* __restrict__ offset,
                        const int* __restrict__ idx, const uint8_t* __restrict__ mask,
                        const int* __restrict__ seq, int64_t T, int S, int E, int K, int chunk,
                        float* __restrict__ psum, int* __restrict__ pcnt, int* __restrict__ pn) {
   using Ring = RowRing<NV, KIND>;
   extern __shared__ __align__(16) float smem_f[];
-  float* red = smem_f + BAL_WARPS * (Ring::BYTES / 4);          // [BAL_WARPS][E]
-  int* hist = reinterpret_cast<int*>(red + BAL_WARPS * E);      // [E]
-  __shared__ int nvalid[BAL_WARPS];
+  float* red = smem_f + W * (Ring::BYTES / 4);          // [W][E]
+  int* hist = reinterpret_cast<int*>(red + W * E);      // [E]
+  __shared__ int nvalid[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
@@ -110,7 +109,7 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
       ring.fetch(logits + f * E, idx + f * K, nullptr, E, K, lane);
     else
       ring.none();
-    f += BAL_WARPS;
+    f += W;
   };
   for (int i = 0; i < Ring::DEPTH - 1; ++i) fetch();
   const Offset<NV, KIND> off(offset, E, lane);
@@ -123,14 +122,14 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
     const int64_t a = sa > t ? sa : t, e = se < t1 ? se : t1;
     if (a >= t1) break;
     if (a >= e) continue;
-    for (int j = threadIdx.x; j < E; j += BAL_THREADS) hist[j] = 0;
+    for (int j = threadIdx.x; j < E; j += W * 32) hist[j] = 0;
     __syncthreads();
     Row<NV> acc;
     acc.fill(0.f);
     int n = 0;
-    for (; u < e; u += BAL_WARPS) {
+    for (; u < e; u += W) {
       if (left == 0) {
-        on = on_bits(mask, u, t1, lane);
+        on = on_bits<W>(mask, u, t1, lane);
         left = 32;
       }
       const bool counts = u >= a && (on & 1u);   // (tokens in a gap before a are passed over)
@@ -155,17 +154,17 @@ balance_partial_kernel(const float* __restrict__ logits, const float* __restrict
     if (lane == 0) nvalid[warp] = n;
     __syncthreads();
     const int64_t at = (static_cast<int64_t>(blockIdx.x) + s) * E;
-    for (int j = threadIdx.x; j < E; j += BAL_THREADS) {
+    for (int j = threadIdx.x; j < E; j += W * 32) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < BAL_WARPS; ++w) sum += red[w * E + j];
+      for (int w = 0; w < W; ++w) sum += red[w * E + j];
       psum[at + j] = sum;
       pcnt[at + j] = hist[j];
     }
     if (threadIdx.x == 0) {
       int m = 0;
 #pragma unroll
-      for (int w = 0; w < BAL_WARPS; ++w) m += nvalid[w];
+      for (int w = 0; w < W; ++w) m += nvalid[w];
       pn[blockIdx.x + s] = m;
     }
     __syncthreads();
@@ -353,7 +352,7 @@ route_backward_kernel(const float* __restrict__ logits, const float* __restrict_
   int left = 0;
   for (int64_t t = t0 + warp; t < t1; t += BAL_WARPS) {
     if (left == 0) {
-      bits = on_bits(mask, t, t1, lane);
+      bits = on_bits<BAL_WARPS>(mask, t, t1, lane);
       left = 32;
     }
     const bool on = bits & 1u;
@@ -455,17 +454,22 @@ cudaError_t launch_balance_loss(const float* logits, const float* offset, const 
   int* pcnt = reinterpret_cast<int*>(ws + pl.cnt_off);
   int* pn = reinterpret_cast<int*>(ws + pl.n_off);
   if (pl.blocks > 0) {
-    const cudaError_t e = with_row_shape(E, [&](auto nv, auto kind) {
+    auto partial = [&](auto nv, auto kind, auto warps) {
       constexpr int NV = decltype(nv)::value;
       constexpr int KIND = decltype(kind)::value;
-      constexpr auto kern = balance_partial_kernel<NV, KIND>;
-      constexpr int ring = BAL_WARPS * RowRing<NV, KIND>::BYTES;
-      const size_t smem = ring + static_cast<size_t>(BAL_WARPS + 1) * E * sizeof(float);
-      const cudaError_t el = smem_limit<kern>(ring + (BAL_WARPS + 1) * NV * 512);
+      constexpr int W = decltype(warps)::value;
+      constexpr auto kern = balance_partial_kernel<NV, KIND, W>;
+      constexpr int ring = W * RowRing<NV, KIND>::BYTES;
+      const size_t smem = ring + static_cast<size_t>(W + 1) * E * sizeof(float);
+      const cudaError_t el = smem_limit<kern>(ring + (W + 1) * NV * 512);
       if (el != cudaSuccess) return el;
-      return launch_pdl(kern, dim3(static_cast<unsigned>(pl.blocks)), dim3(BAL_THREADS), smem,
-                        stream, logits, offset, idx, mask, seq, T, S, E, K, pl.chunk, psum, pcnt,
-                        pn);
+      return launch_pdl(kern, dim3(static_cast<unsigned>(pl.blocks)), dim3(W * 32), smem, stream,
+                        logits, offset, idx, mask, seq, T, S, E, K, pl.chunk, psum, pcnt, pn);
+    };
+    const cudaError_t e = with_row_shape(E, [&](auto nv, auto kind) {
+      if constexpr (decltype(nv)::value > 3)
+        if (pl.warps == 2 * BAL_WARPS) return partial(nv, kind, IntC<2 * BAL_WARPS>{});
+      return partial(nv, kind, IntC<BAL_WARPS>{});
     });
     if (e != cudaSuccess) return e;
   }

@@ -52,14 +52,22 @@ cudaError_t launch_route_logits(const float* logits, const float* b, const float
 struct BalancePlan {
   int64_t blocks;
   int chunk;
+  int warps;         // of a block
   size_t cnt_off, n_off, bytes;
 };
+constexpr int BAL_WARPS = 8;
 constexpr int bal_blocks(int nv) { return nv <= 3 ? 3 : 2; }   // nv = ceil(E / 128)
 inline BalancePlan balance_plan(int64_t T, int S, int E) {
   BalancePlan p;
-  const int grid = bal_blocks((E + 127) / 128) * 148;
+  const int nv = (E + 127) / 128;
+  // Long rows of few long sequences: blocks of 16 warps, one per SM, leave half the
+  // sums to add (16384 x 768 in 4: 16.0 -> 15.5 us, 5000 x 768 13.0 -> 11.0); with
+  // many sequences twice the warps wait at every end (in 50: 15.9 -> 16.2).
+  const bool wide = nv > 3 && S <= 8 && T >= 2 * 148 * 2 * BAL_WARPS;
+  p.warps = wide ? 2 * BAL_WARPS : BAL_WARPS;
+  const int grid = (wide ? 1 : bal_blocks(nv)) * 148;
   const int64_t want = (T + grid - 1) / grid;
-  p.chunk = static_cast<int>(want < 8 ? 8 : want);
+  p.chunk = static_cast<int>(want < p.warps ? p.warps : want);
   // (a few more tokens a block rather than more partial sums to add: 4096 x 96
   // 9.3 -> 7.5 us)
   if (p.chunk > 8 && p.chunk < 16) p.chunk = 16;

@@ -76,6 +76,21 @@ def test_balance_loss_lengths(T):
     check_balance(mz.balance_loss(logits, idx, seq_start=s), logits, idx, seq=s)
 
 
+@pytest.mark.parametrize("E,K,T,seq", [
+    (8, 2, 20000, None), (33, 3, 9000, [0, 4000, 9000]), (96, 6, 4096, None), (250, 4, 8192, [0, 3000, 3000, 8000]),
+    (384, 5, 6000, None), (385, 5, 4736, None), (500, 3, 4800, [0, 100, 4000, 4790]), (640, 4, 4740, [3, 4, 4700]),
+    (768, 12, 5003, [0, 1000, 1001, 2000, 3000, 4000, 4500, 5000, 5003]), (768, 12, 4735, None), (1021, 9, 4799, None), (1024, 32, 5000, [0, 0, 2500, 4990]),
+])
+@pytest.mark.parametrize("masked", [False, True])
+def test_balance_loss_many_rows_to_add(E, K, T, seq, masked):
+    logits, idx = rows_case(T, E, K, seed=T)
+    kw = dict(mask=(torch.rand(T, generator=gen(E)) < 0.7).cuda()) if masked else {}
+    if seq is not None:
+        kw["seq"] = ints(seq)
+    r = mz.balance_loss(logits, idx, mask=kw.get("mask"), seq_start=kw.get("seq"))
+    check_balance(r, logits, idx, **kw)
+
+
 def test_balance_loss_a_sequence_per_token():
     T = 1500
     logits, idx = rows_case(T, 40, 4)
