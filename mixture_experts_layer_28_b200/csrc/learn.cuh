@@ -46,9 +46,9 @@ cudaError_t launch_route_logits(const float* logits, const float* b, const float
 // The balance loss (balance.cu).  Tokens are cut into `blocks` ranges of
 // `chunk`; its workspace holds, for each of blocks + S (range, sequence)
 // slots, E partial sums, E partial counts and the number of counted tokens.
-// One wave of resident blocks on the 148 multiprocessors of a B200 (three per
-// multiprocessor up to 384 experts, else two), each with at least one token per
-// warp.
+// One wave of resident blocks on the 148 multiprocessors of a B200 (of 8 warps, three
+// per multiprocessor up to 384 experts, else two; or one of 16 warps), each with at
+// least one token per warp.
 struct BalancePlan {
   int64_t blocks;
   int chunk;
