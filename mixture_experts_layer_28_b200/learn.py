@@ -72,6 +72,7 @@ class RouterStep:
         self._saved = (x, logits, idx, gate, slot, y, mask, seq_start, logit_offset)
         return mz.combine(x, y, slot, gate, zsum)
 
+    @torch.no_grad()
     def backward(self, dout: torch.Tensor) -> RouterGrad:
         """Gradient of W_r from the output's gradient dout bf16 [T, d] and the
         balance loss; consumes what forward kept."""

@@ -418,7 +418,8 @@ def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: torch.Tensor, N: int, Z:
 
 
 class BalanceLoss(NamedTuple):
-    """What moe_zc_balance_loss computes."""
+    """What moe_zc_balance_loss computes: views of one buffer, in which the call's
+    workspace lies too (clone what is kept over many steps)."""
     loss: torch.Tensor      # fp32 [S]
     counts: torch.Tensor    # int32 [S, E]: counted tokens' picks per expert
     prob: torch.Tensor      # fp32 [S, E]: mean router probability

@@ -203,3 +203,18 @@ def test_all_picks_on_zero_experts():
     err = ((UB + rel) * dl).t() @ xc.abs() + p.t() @ (xc.abs() * 4 * d * U * (xc * dc).abs().sum(1, keepdim=True)) * 2
     err = err + UB * want.abs() + T * U * (dl.t() @ xc.abs())
     assert ((g.W_r.double().cpu() - want).abs() <= err).all()
+
+
+def test_inputs_of_an_autograd_graph():
+    W_r, b, Wg, Wu, Wd, x, dout = layer(4, 2, 2, 256, 128, 30)
+    want = learn.RouterStep(4, 2, 2, W_r.clone(), b, Wg, Wu, Wd, lr=1e-2)
+    want.forward(x)
+    w = want.backward(dout).W_r
+    W_r.requires_grad_()
+    st = learn.RouterStep(4, 2, 2, W_r, b, Wg, Wu, Wd, lr=1e-2)
+    y = (x.requires_grad_() * 1.0)
+    assert not st.forward(y).requires_grad
+    g = st.backward(dout)
+    assert torch.equal(g.W_r, w) and not g.W_r.requires_grad
+    st.step(g.W_r)
+    assert torch.equal(W_r.detach(), st.opt.master[0].to(torch.bfloat16))
